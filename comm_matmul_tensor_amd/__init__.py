@@ -12,6 +12,7 @@ Functions carry the C names:
   mc2_alltoall_quant_matmul_workspace_size, mc2_alltoall_quant_matmul, mc2_alltoall_quant_matmul_static,
   mc2_alltoall_quant_matmul_noalloc, mc2_alltoall_quant_matmul_a16w4, mc2_alltoall_quant_matmul_a4w4,
   mc2_quant_all_reduce, mc2_quant_reduce_scatter, mc2_status_string, mc2_last_error;
+the feed-forward operators of include/mc2_layer.h (layer.py);
 and the test hook mc2_testing_arrival (csrc/testing.h, outside the public header).
 
 Every call checks each tensor's shape, dtype and device against the sizes it
@@ -666,3 +667,8 @@ __all__ = [
     "mc2_quant_all_reduce", "mc2_quant_reduce_scatter",
     "mc2_status_string", "mc2_last_error", "Mc2Error", "LIB_PATH",
 ]
+
+from . import layer as _layer  # noqa: E402  (uses the names above)
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += _layer.__all__

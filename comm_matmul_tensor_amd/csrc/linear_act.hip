@@ -1,0 +1,414 @@
+// K11, around the tiled product: the plan of a call (tile, split, workspace),
+// the product of few rows, the gradient's dz and bias sums, and the copies
+// that give rows of a ragged width an aligned one.
+#include <algorithm>
+
+#include "linear_kernels.hpp"
+
+namespace mc2 {
+namespace lin {
+
+Plan plan_product(int64_t m, int64_t n, int64_t k, int gmode, int64_t groups) {
+  auto tiles = [&](int64_t t) {
+    const int64_t per_rows = (m + t - 1) / t, cols = (n + t - 1) / t;
+    // (an upper bound for groups of rows, where each group's last tile may be partial)
+    if (gmode == BY_ROWS) return (per_rows + groups) * cols;
+    return per_rows * cols * (gmode == BY_K ? groups : 1);
+  };
+  Plan p{128, 1, k, 0};
+  const int64_t t256 = tiles(256), t128 = tiles(128);
+  const int64_t rows_each = gmode == BY_ROWS ? m / groups : m;
+  // passes over the 256 CUs in units of a 128-tile: a 256-tile takes four, two
+  // 128-tiles share a CU (and one alone leaves part of it idle)
+  const double cost256 = 4.0 * (double)((t256 + 255) / 256);
+  const int64_t rest = t128 % 512;
+  const double cost128 = 2.3 * (double)(t128 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.4 : 2.3);
+  if (cost256 < cost128 && rows_each >= 192) {
+    p.tile = 256;
+    return p;
+  }
+  if (gmode == DENSE && t128 <= 256 && k >= 512) {
+    int64_t s = std::min<int64_t>({512 / std::max<int64_t>(t128, 1), k / 256, 32});
+    if (s > 1) {
+      p.k_part = ((k + s - 1) / s + kStepK - 1) / kStepK * kStepK;
+      p.splits = (int)((k + p.k_part - 1) / p.k_part);
+      if (p.splits > 1)
+        p.partial_bytes = (size_t)p.splits * ((m + 127) / 128 * 128) * ((n + 127) / 128 * 128) * sizeof(float);
+    }
+  }
+  return p;
+}
+
+namespace {
+
+int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// ---------------------------------------------------------------- ragged rows
+// dst (rows, ld) = src (rows, k) with zeros in columns k .. ld - 1.
+__global__ __launch_bounds__(256) void pad_rows(const uint16_t* src, int64_t rows, int64_t k, int64_t ld,
+                                                uint16_t* dst) {
+  const int64_t chunks = ld / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * chunks; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / chunks, c = i % chunks * 8;
+    *reinterpret_cast<u32x4*>(dst + row * ld + c) = load_chunk<false>(src + row * k, c, k);
+  }
+}
+hipError_t launch_pad_rows(const void* src, int64_t rows, int64_t k, void* dst, hipStream_t s) {
+  const int64_t chunks = rows * (pad8(k) / 8);
+  if (chunks == 0) return hipSuccess;
+  pad_rows<<<(unsigned)std::min<int64_t>((chunks + 255) / 256, 256 * 16), 256, 0, s>>>(
+      static_cast<const uint16_t*>(src), rows, k, pad8(k), static_cast<uint16_t*>(dst));
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- few rows
+// m <= 16 MF rows (a decoding step): bound by reading w once.  A workgroup
+// makes 16 columns of C; its WAVES wavefronts take K in turn, 32 U at a time,
+// and their sums are added in wavefront order.  An MFMA takes 16 rows of w
+// (its first operand) and 16 rows of x (rows past m repeat the last one and
+// are not stored); fragments come straight from memory, U of each in flight.
+constexpr int kSkinnyU = 8;
+template <int DT, int MF, int WAVES, bool VEC>
+__global__ __launch_bounds__(64 * WAVES) void skinny_kernel(Product p) {
+  __shared__ float red[WAVES][MF * 256];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t n0 = (int64_t)blockIdx.x * 16, k = p.k;
+  const int64_t wr = n0 + lane % 16 < p.n ? n0 + lane % 16 : p.n - 1;
+  const uint16_t* w = static_cast<const uint16_t*>(p.b) + wr * k;
+  const uint16_t* x[MF];
+  f32x4 acc[MF];
+#pragma unroll
+  for (int i = 0; i < MF; i++) {
+    const int64_t r = 16 * i + lane % 16 < p.m ? 16 * i + lane % 16 : p.m - 1;
+    x[i] = static_cast<const uint16_t*>(p.a) + r * k;
+    acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  for (int64_t kb = (int64_t)wave * 32 * kSkinnyU; kb < k; kb += (int64_t)WAVES * 32 * kSkinnyU) {
+    u32x4 fw[kSkinnyU], fx[MF][kSkinnyU];
+#pragma unroll
+    for (int u = 0; u < kSkinnyU; u++) {
+      const int64_t c = kb + 32 * u + 8 * (lane / 16);
+      fw[u] = u32x4{0u, 0u, 0u, 0u};
+      if (c < k) fw[u] = load_chunk<VEC>(w, c, k);
+#pragma unroll
+      for (int i = 0; i < MF; i++) {
+        fx[i][u] = u32x4{0u, 0u, 0u, 0u};
+        if (c < k) fx[i][u] = load_chunk<VEC>(x[i], c, k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSkinnyU; u++)
+#pragma unroll
+      for (int i = 0; i < MF; i++) acc[i] = mfma16<DT>(fw[u], fx[i][u], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < MF; i++)
+    *reinterpret_cast<f32x4*>(&red[wave][256 * i + lane % 16 * 16 + 4 * (lane / 16)]) = acc[i];
+  __syncthreads();
+  for (int t = threadIdx.x; t < MF * 256; t += 64 * WAVES) {
+    const int64_t row = t / 16, col = n0 + t % 16;
+    if (row >= p.m || col >= p.n) continue;
+    float v = red[0][t];
+#pragma unroll
+    for (int s = 1; s < WAVES; s++) v += red[s][t];
+    if (p.bias) v += dec16<DT>(static_cast<const uint16_t*>(p.bias)[col]);
+    const int64_t at = row * p.n + col;
+    if (p.z) static_cast<uint16_t*>(p.z)[at] = enc16<DT>(v);
+    with_act(p.act, [&](auto ACT_) { v = act_of<decltype(ACT_)::value>(v); });
+    if (p.residual) v += dec16<DT>(static_cast<const uint16_t*>(p.residual)[at]);
+    static_cast<uint16_t*>(p.out)[at] = enc16<DT>(v);
+  }
+}
+
+constexpr int64_t kSkinnyRows = 32;
+
+template <int DT, int MF>
+hipError_t launch_skinny(const Product& p, hipStream_t s) {
+  const unsigned blocks = (unsigned)((p.n + 15) / 16);
+  const bool vec = p.k % 8 == 0;
+  // enough wavefronts in flight to cover HBM's latency: 4 a workgroup where
+  // the columns make 256 workgroups, else 16
+  if (blocks >= 256) {
+    if (vec) skinny_kernel<DT, MF, 4, true><<<blocks, 256, 0, s>>>(p);
+    else skinny_kernel<DT, MF, 4, false><<<blocks, 256, 0, s>>>(p);
+  } else {
+    if (vec) skinny_kernel<DT, MF, 16, true><<<blocks, 1024, 0, s>>>(p);
+    else skinny_kernel<DT, MF, 16, false><<<blocks, 1024, 0, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- dz and bias sums
+// dz = dout act'(z) for a tile of 64 rows (of one group) x 256 columns, and
+// the column sums of the unrounded dz over the tile's rows: thread (r, c) of
+// 8 x 32 takes rows r, r + 8, ... and 8 columns; the 8 rows' sums are added
+// in order.
+constexpr int kDzRows = 64, kDzCols = 256;
+struct DzArgs {
+  const uint16_t *dout, *z;
+  uint16_t* dz;    // (m, ld) or NULL
+  float* partial;  // (row tiles, n) or NULL
+  int64_t m, n, ld;
+  const int32_t* offsets;
+  int64_t groups;
+};
+template <int DT, int ACT, bool VEC>
+__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+  __shared__ float red[8][kDzCols + 8];
+  int64_t m0 = (int64_t)blockIdx.x * kDzRows, m_end = a.m;
+  if (a.groups > 0) {
+    const RowRange r = find_tile(a.offsets, a.groups, a.m, kDzRows, blockIdx.x);
+    if (r.group == a.groups) return;
+    m0 = r.begin + r.tile * kDzRows;
+    m_end = r.end;
+  }
+  if (m0 + kDzRows < m_end) m_end = m0 + kDzRows;
+  const int rt = threadIdx.x / 32, ct = threadIdx.x % 32;
+  const int64_t c = (int64_t)blockIdx.y * kDzCols + 8 * ct;
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (c < a.n) {
+#pragma unroll 4
+    for (int64_t row = m0 + rt; row < m_end; row += 8) {
+      float d[8];
+      unpack8<DT>(load_chunk<VEC>(a.dout + row * a.n, c, a.n), d);
+      if constexpr (ACT != ACT_NONE) {
+        float f[8];
+        unpack8<DT>(load_chunk<VEC>(a.z + row * a.n, c, a.n), f);
+#pragma unroll
+        for (int e = 0; e < 8; e++) d[e] *= act_slope<ACT>(f[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        if (!VEC && c + e >= a.n) d[e] = 0.0f;
+        sum[e] += d[e];
+      }
+      if (a.dz) *reinterpret_cast<u32x4*>(a.dz + row * a.ld + c) = pack8<DT>(d);
+    }
+  }
+  if (!a.partial) return;
+#pragma unroll
+  for (int e = 0; e < 8; e++) red[rt][8 * ct + e] = sum[e];
+  __syncthreads();
+  const int64_t col = (int64_t)blockIdx.y * kDzCols + threadIdx.x;
+  if (col >= a.n) return;
+  float s = red[0][threadIdx.x];
+#pragma unroll
+  for (int r = 1; r < 8; r++) s += red[r][threadIdx.x];
+  a.partial[(int64_t)blockIdx.x * a.n + col] = s;
+}
+
+// dbias[g][j] = sum of the partial sums of group g's row tiles, in order within
+// each of 4 wavefronts and over them.
+template <int DT>
+__global__ __launch_bounds__(256) void dbias_kernel(DzArgs a, int64_t tiles, uint16_t* dbias) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int64_t j = (int64_t)blockIdx.x * 64 + lane;
+  int64_t first = 0, count = tiles;
+  if (a.groups > 0) {  // tiles of the groups before this one, and its own
+    const int64_t g = blockIdx.y;
+    int64_t begin = 0;
+    count = 0;
+    for (int64_t i = 0; i <= g; i++) {
+      int64_t end = a.offsets[i + 1];
+      end = end < begin ? begin : end > a.m ? a.m : end;
+      first += count;
+      count = (end - begin + kDzRows - 1) / kDzRows;
+      begin = end;
+    }
+    dbias += g * a.n;
+  }
+  float s = 0.0f;
+  if (j < a.n) {
+#pragma unroll 4
+    for (int64_t t = first + wave; t < first + count; t += 4) s += a.partial[t * a.n + j];
+  }
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && j < a.n) dbias[j] = enc16<DT>(((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane]);
+}
+
+int64_t dz_tiles(int64_t m, int64_t groups) { return (m + kDzRows - 1) / kDzRows + groups; }
+
+template <int DT>
+hipError_t launch_dz(const DzArgs& a, int act, void* dbias, hipStream_t s) {
+  const int64_t tiles = dz_tiles(a.m, a.groups);
+  const bool vec = a.n % 8 == 0;
+  if (a.m > 0 && (a.dz || dbias)) {
+    const dim3 grid((unsigned)tiles, (unsigned)((a.n + kDzCols - 1) / kDzCols));
+    with_act(act, [&](auto ACT_) {
+      constexpr int ACT = decltype(ACT_)::value;
+      if (vec) dz_kernel<DT, ACT, true><<<grid, 256, 0, s>>>(a);
+      else dz_kernel<DT, ACT, false><<<grid, 256, 0, s>>>(a);
+    });
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (dbias) {
+    const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)std::max<int64_t>(a.groups, 1));
+    dbias_kernel<DT><<<grid, 256, 0, s>>>(a, tiles, static_cast<uint16_t*>(dbias));
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+// Parts of a workspace, in order, each 256-byte aligned.
+struct Parts {
+  size_t used = 0;
+  size_t take(size_t bytes) {
+    const size_t at = used;
+    used += up256(bytes);
+    return at;
+  }
+};
+
+struct ForwardLayout {
+  size_t x8, w8, partial, total;
+  Plan plan;
+  ForwardLayout(int64_t m, int64_t k, int64_t n, int64_t groups) {
+    Parts p;
+    plan = plan_product(m, n, k, groups ? BY_ROWS : DENSE, groups);
+    const bool skinny = !groups && m <= kSkinnyRows, ragged = k % 8 != 0 && !skinny;
+    x8 = p.take(ragged ? (size_t)m * pad8(k) * 2 : 0);
+    w8 = p.take(ragged ? (size_t)std::max<int64_t>(groups, 1) * n * pad8(k) * 2 : 0);
+    partial = p.take(skinny ? 0 : plan.partial_bytes);
+    total = p.used;
+  }
+};
+
+struct GradLayout {
+  size_t dz, sums, x8, w8, partial, total;
+  Plan dx, dw;
+  GradLayout(int64_t m, int64_t k, int64_t n, int64_t groups) {
+    Parts p;
+    dx = plan_product(m, k, n, groups ? BY_ROWS : DENSE, groups);
+    dw = plan_product(n, k, m, groups ? BY_K : DENSE, groups);
+    dz = p.take((size_t)m * pad8(n) * 2);
+    sums = p.take((size_t)dz_tiles(m, groups) * n * sizeof(float));
+    x8 = p.take(k % 8 ? (size_t)m * pad8(k) * 2 : 0);
+    w8 = p.take(k % 8 ? (size_t)std::max<int64_t>(groups, 1) * n * pad8(k) * 2 : 0);
+    partial = p.take(std::max(dx.partial_bytes, dw.partial_bytes));
+    total = p.used;
+  }
+};
+
+template <int DT>
+hipError_t forward_dt(const LinearArgs& a, hipStream_t s) {
+  const ForwardLayout at(a.m, a.k, a.n, a.groups);
+  char* ws = static_cast<char*>(a.workspace);
+  Product p{};
+  p.a = a.x;
+  p.b = a.w;
+  p.m = a.m;
+  p.n = a.n;
+  p.k = a.k;
+  p.offsets = a.offsets;
+  p.groups = a.groups;
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.out = a.out;
+  p.z = a.z;
+  p.act = a.act;
+  p.splits = 1;
+  if (!a.groups && a.m <= kSkinnyRows)
+    return a.m <= 16 ? launch_skinny<DT, 1>(p, s) : launch_skinny<DT, 2>(p, s);
+  p.lda = p.ldb = pad8(a.k);
+  p.b_group = a.n * p.ldb;
+  if (a.k % 8) {
+    hipError_t e = launch_pad_rows(a.x, a.m, a.k, ws + at.x8, s);
+    if (e == hipSuccess) e = launch_pad_rows(a.w, std::max<int64_t>(a.groups, 1) * a.n, a.k, ws + at.w8, s);
+    if (e != hipSuccess) return e;
+    p.a = ws + at.x8;
+    p.b = ws + at.w8;
+  }
+  p.partial = reinterpret_cast<float*>(ws + at.partial);
+  return launch_product<DT>(p, 0, a.groups ? BY_ROWS : DENSE, at.plan, s);
+}
+
+template <int DT>
+hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
+  const GradLayout at(a.m, a.k, a.n, a.groups);
+  char* ws = static_cast<char*>(a.workspace);
+  const int64_t matrices = std::max<int64_t>(a.groups, 1);
+  // dz: dout itself without an activation, where its rows are aligned
+  const bool products = a.dx || a.dw, copy = a.act != ACT_NONE || a.n % 8 != 0;
+  DzArgs d{};
+  d.dout = static_cast<const uint16_t*>(a.dout);
+  d.z = static_cast<const uint16_t*>(a.z);
+  d.dz = products && copy ? reinterpret_cast<uint16_t*>(ws + at.dz) : nullptr;
+  d.partial = a.dbias ? reinterpret_cast<float*>(ws + at.sums) : nullptr;
+  d.m = a.m;
+  d.n = a.n;
+  d.ld = pad8(a.n);
+  d.offsets = a.offsets;
+  d.groups = a.groups;
+  hipError_t e = launch_dz<DT>(d, a.act, a.dbias, s);
+  if (e != hipSuccess || !products) return e;
+  const void *x = a.x, *w = a.w, *dz = copy ? d.dz : a.dout;
+  if (a.k % 8) {
+    if (a.dw) {
+      e = launch_pad_rows(a.x, a.m, a.k, ws + at.x8, s);
+      x = ws + at.x8;
+    }
+    if (e == hipSuccess && a.dx) {
+      e = launch_pad_rows(a.w, matrices * a.n, a.k, ws + at.w8, s);
+      w = ws + at.w8;
+    }
+    if (e != hipSuccess) return e;
+  }
+  Product p{};
+  p.offsets = a.offsets;
+  p.groups = a.groups;
+  p.act = ACT_NONE;
+  p.partial = reinterpret_cast<float*>(ws + at.partial);
+  if (a.dx && a.m > 0) {  // (m, k) = dz (m, n) @ w (n, k)
+    p.a = dz;
+    p.lda = pad8(a.n);
+    p.b = w;
+    p.ldb = pad8(a.k);
+    p.b_group = a.n * p.ldb;
+    p.m = a.m;
+    p.n = a.k;
+    p.k = a.n;
+    p.out = a.dx;
+    e = launch_product<DT>(p, 1, a.groups ? BY_ROWS : DENSE, at.dx, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.dw) {  // (n, k) = dz (m, n)^T @ x (m, k)
+    p.a = dz;
+    p.lda = pad8(a.n);
+    p.b = x;
+    p.ldb = pad8(a.k);
+    p.b_group = 0;
+    p.m = a.n;
+    p.n = a.k;
+    p.k = a.m;
+    p.out = a.dw;
+    e = launch_product<DT>(p, 2, a.groups ? BY_K : DENSE, at.dw, s);
+  }
+  return e;
+}
+
+}  // namespace
+}  // namespace lin
+
+size_t linear_act_workspace(int64_t m, int64_t k, int64_t n, int64_t groups) {
+  return m > 0 ? lin::ForwardLayout(m, k, n, groups).total : 0;
+}
+size_t linear_act_grad_workspace(int64_t m, int64_t k, int64_t n, int64_t groups) {
+  return lin::GradLayout(m, k, n, groups).total;
+}
+
+hipError_t launch_linear_act(const LinearArgs& a, hipStream_t s) {
+  if (a.m < 1 || a.k < 1 || a.n < 1 || a.groups < 0 || a.k > lin::kMaxDim || a.n > lin::kMaxDim)
+    return hipErrorInvalidValue;
+  return a.dtype == DT_BF16 ? lin::forward_dt<DT_BF16>(a, s) : lin::forward_dt<DT_F16>(a, s);
+}
+hipError_t launch_linear_act_grad(const LinearGradArgs& a, hipStream_t s) {
+  if (a.m < 0 || a.k < 1 || a.n < 1 || a.groups < 0 || a.k > lin::kMaxDim || a.n > lin::kMaxDim)
+    return hipErrorInvalidValue;
+  return a.dtype == DT_BF16 ? lin::grad_dt<DT_BF16>(a, s) : lin::grad_dt<DT_F16>(a, s);
+}
+
+}  // namespace mc2

@@ -1,0 +1,85 @@
+// Activations of the linear's epilogue and their slopes, in fp32.
+//
+// An epilogue runs them on every element of C between the product's last MFMA
+// and its stores, with nothing to hide behind, so each takes one exponential
+// (v_exp_f32) and at most one reciprocal (v_rcp_f32), about 1 ulp each, far
+// below the 16-bit rounding that follows.
+//
+// Phi(z), the normal distribution function, is Abramowitz and Stegun's
+// formula 7.1.26 for erfc (Handbook of Mathematical Functions, 1964; absolute
+// error below 1.5e-7): for x >= 0,
+//   erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-x^2), t = 1 / (1 + p x),
+// and Phi(z) = erfc(-z / sqrt 2) / 2.  The negative side uses it directly, so
+// it does not cancel.
+#pragma once
+#include "layer_device.hpp"
+
+namespace mc2 {
+
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// exp(-z^2 / 2) and Phi(z)
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = __builtin_fabsf(z) * 0.70710678118654752440f;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+  e = __builtin_amdgcn_exp2f(-kLog2e * (x * x));
+  float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
+  q = __builtin_fmaf(t, q, 1.421413741f);
+  q = __builtin_fmaf(t, q, -0.284496736f);
+  q = __builtin_fmaf(t, q, 0.254829592f);
+  q = 0.5f * (q * t) * e;
+  return z > 0.0f ? 1.0f - q : q;
+}
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
+constexpr float kTanhA = 1.59576912160573071176f;            // 2 sqrt(2 / pi)
+constexpr float kTanhB = 1.59576912160573071176f * 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
+  if constexpr (ACT == ACT_GELU) {
+    float e;
+    return z * normal_cdf(z, e);
+  }
+  // 0.5 (1 + tanh u) = sigmoid(2 u)
+  if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid(z * __builtin_fmaf(kTanhB, z * z, kTanhA));
+  if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if constexpr (ACT == ACT_GELU) {
+    float e;
+    const float p = normal_cdf(z, e);
+    return __builtin_fmaf(z * 0.39894228040143267794f, e, p);
+  }
+  if constexpr (ACT == ACT_GELU_TANH) {
+    const float p = sigmoid(z * __builtin_fmaf(kTanhB, z * z, kTanhA));
+    return __builtin_fmaf(z * p * (1.0f - p), __builtin_fmaf(3.0f * kTanhB, z * z, kTanhA), p);
+  }
+  if constexpr (ACT == ACT_SILU) {
+    const float p = sigmoid(z);
+    return __builtin_fmaf(z * p, 1.0f - p, p);
+  }
+  return 1.0f;
+}
+
+// Calls f with the activation as a compile-time constant.
+template <typename F>
+__host__ __device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case ACT_RELU: f(std::integral_constant<int, ACT_RELU>()); break;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>()); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>()); break;
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>()); break;
+    default: f(std::integral_constant<int, ACT_NONE>());
+  }
+}
+
+}  // namespace mc2

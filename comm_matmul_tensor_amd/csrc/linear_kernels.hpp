@@ -1,0 +1,26 @@
+// Launches shared by the linear's translation units: the tiled product
+// (gemm_linear_bf16.hip, gemm_linear_f16.hip) and the plan it follows.
+#pragma once
+#include "linear_gemm.hpp"
+
+namespace mc2 {
+namespace lin {
+
+// Tile and split of a product, from its sizes alone (the workspace's size
+// follows it).
+struct Plan {
+  int tile;          // 256 or 128
+  int splits;        // parts of K (dense only), each k_part long
+  int64_t k_part;
+  size_t partial_bytes;
+};
+Plan plan_product(int64_t m, int64_t n, int64_t k, int gmode, int64_t groups);
+
+// Layout: 0 A K-, B K-contiguous (forward); 1 A K-, B N-contiguous (dx);
+// 2 A M-, B N-contiguous (dw).  The product's splits, k_part, partial, order
+// and epilogue are set here from the plan.
+template <int DT>
+hipError_t launch_product(const Product& p, int layout, int gmode, const Plan& plan, hipStream_t s);
+
+}  // namespace lin
+}  // namespace mc2
