@@ -45,7 +45,7 @@ __global__ __launch_bounds__(256) void join_kernel(Product p, int64_t ld, int64_
   store(out, v);
 }
 
-template <int DT, int BM, int BN, int WGM, int WGN, bool AK, bool BK, int GMODE>
+template <int DT, int BM, int BN, int WGM, int WGN, int NS, bool AK, bool BK, int GMODE>
 hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
   const int64_t tiles_m = (p.m + BM - 1) / BM + (GMODE == BY_ROWS ? p.groups : 0), tiles_n = (p.n + BN - 1) / BN;
   p.splits = plan.splits;
@@ -53,7 +53,7 @@ hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
   p.order_cols = gemm::prefer_column_order(p.m, p.n, p.k, 2) ? 1 : 0;
   p.tile_group = gemm::choose_tile_group(tiles_m * BM, p.n, BM, BN, p.order_cols);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)(GMODE == BY_K ? p.groups : plan.splits));
-  product_kernel<DT, BM, BN, WGM, WGN, AK, BK, GMODE><<<grid, 64 * WGM * WGN, 0, s>>>(p);
+  product_kernel<DT, BM, BN, WGM, WGN, NS, AK, BK, GMODE><<<grid, 64 * WGM * WGN, 0, s>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.splits < 2) return e;
   const int64_t ld = tiles_n * BN;
@@ -64,8 +64,11 @@ hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
 
 template <int DT, bool AK, bool BK, int GMODE>
 hipError_t launch_layout(const Product& p, const Plan& plan, hipStream_t s) {
-  if (plan.tile == 256) return launch_tile<DT, 256, 256, 2, 4, AK, BK, GMODE>(p, plan, s);
-  return launch_tile<DT, 128, 128, 2, 2, AK, BK, GMODE>(p, plan, s);
+  switch (plan.tile) {
+    case TILE_256X256: return launch_tile<DT, 256, 256, 2, 4, 2, AK, BK, GMODE>(p, plan, s);
+    case TILE_128X256: return launch_tile<DT, 128, 256, 2, 4, 3, AK, BK, GMODE>(p, plan, s);
+    default: return launch_tile<DT, 128, 128, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+  }
 }
 
 }  // namespace

@@ -2,6 +2,7 @@
 // the product of few rows, the gradient's dz and bias sums, and the copies
 // that give rows of a ragged width an aligned one.
 #include <algorithm>
+#include <cmath>
 
 #include "linear_kernels.hpp"
 
@@ -9,32 +10,28 @@ namespace mc2 {
 namespace lin {
 
 Plan plan_product(int64_t m, int64_t n, int64_t k, int gmode, int64_t groups) {
-  auto tiles = [&](int64_t t) {
-    const int64_t per_rows = (m + t - 1) / t, cols = (n + t - 1) / t;
-    // (an upper bound for groups of rows, where each group's last tile may be partial)
-    if (gmode == BY_ROWS) return (per_rows + groups) * cols;
-    return per_rows * cols * (gmode == BY_K ? groups : 1);
+  // turns of the 256 CUs times the time of one (linear_kernels.hpp), the
+  // groups' partial tiles taken as half of one each
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    const double cols = (double)((n + bn - 1) / bn);
+    if (gmode == BY_ROWS) return ((double)m / (double)bm + 0.5 * (double)groups) * cols;
+    return (double)((m + bm - 1) / bm) * cols * (gmode == BY_K ? (double)groups : 1.0);
   };
-  Plan p{128, 1, k, 0};
-  const int64_t t256 = tiles(256), t128 = tiles(128);
-  const int64_t rows_each = gmode == BY_ROWS ? m / groups : m;
-  // passes over the 256 CUs in units of a 128-tile: a 256-tile takes four, two
-  // 128-tiles share a CU (and one alone leaves part of it idle)
-  const double cost256 = 4.0 * (double)((t256 + 255) / 256);
-  const int64_t rest = t128 % 512;
-  const double cost128 = 2.3 * (double)(t128 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.4 : 2.3);
-  if (cost256 < cost128 && rows_each >= 192) {
-    p.tile = 256;
-    return p;
-  }
-  if (gmode == DENSE && t128 <= 256 && k >= 512) {
-    int64_t s = std::min<int64_t>({512 / std::max<int64_t>(t128, 1), k / 256, 32});
-    if (s > 1) {
-      p.k_part = ((k + s - 1) / s + kStepK - 1) / kStepK * kStepK;
-      p.splits = (int)((k + p.k_part - 1) / p.k_part);
-      if (p.splits > 1)
-        p.partial_bytes = (size_t)p.splits * ((m + 127) / 128 * 128) * ((n + 127) / 128 * 128) * sizeof(float);
-    }
+  auto cost = [&](int64_t bm, int64_t bn, double turn) { return std::ceil(tiles(bm, bn) / 256.0) * turn; };
+  const double c256 = cost(256, 256, 95.0), c128 = cost(128, 256, 56.0), small = cost(128, 128, 32.0);
+  Plan p{TILE_128X128, 1, k, 0};
+  if (c256 <= c128 && c256 <= small) p.tile = TILE_256X256;
+  else if (c128 <= small) p.tile = TILE_128X256;
+  if (p.tile != TILE_128X128 || gmode != DENSE) return p;
+  // split K where the tiles leave more than half of the CUs idle, in parts of
+  // 256 at least
+  const int64_t t = (int64_t)tiles(128, 128);
+  const int64_t s = std::min<int64_t>({256 / std::max<int64_t>(t, 1), k / 256, 32});
+  if (s > 1) {
+    p.k_part = ((k + s - 1) / s + kStepK - 1) / kStepK * kStepK;
+    p.splits = (int)((k + p.k_part - 1) / p.k_part);
+    if (p.splits > 1)
+      p.partial_bytes = (size_t)p.splits * ((m + 127) / 128 * 128) * ((n + 127) / 128 * 128) * sizeof(float);
   }
   return p;
 }

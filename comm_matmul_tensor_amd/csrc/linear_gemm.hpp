@@ -66,29 +66,56 @@ struct RowRange { int64_t group, begin, end, tile; };
 // loop bounds made from it need no loop over lanes).
 __device__ __forceinline__ int64_t uniform(int64_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
 
-// Tile `tile` of the ranges cut into tiles of bm rows, counted group by group
-// and then over the rows after the last group (group = groups).  Every
-// wavefront finds it for itself, 64 groups at a time: range ends are read as
-// ascending and at most m.  tile past them all: begin = end = m.
+// 64 groups from g0 on, one per lane: the rows [start, end) of the lane's
+// group and its tiles of bm rows.  Range ends are read as ascending and at
+// most m; `begin`, the end of the group before g0, becomes that of the last.
+struct GroupTiles {
+  int64_t start, end;
+  int tiles;
+  __device__ __forceinline__ GroupTiles(const int32_t* offsets, int64_t groups, int64_t m, int bm, int64_t g0,
+                                        int64_t& begin) {
+    const int lane = threadIdx.x % 64;
+    int e = g0 + lane < groups ? offsets[g0 + lane + 1] : 0;
+    const int b = (int)begin;
+    e = e < b ? b : e > (int)m ? (int)m : e;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(e, d);
+      if (lane >= d && v > e) e = v;
+    }
+    int s = __shfl_up(e, 1);
+    if (lane == 0) s = b;
+    start = s;
+    end = e;
+    tiles = (e - s + bm - 1) / bm;
+    begin = uniform(__shfl(e, 63));
+  }
+};
+
+// Tiles of bm rows over all groups (each counts its own) and over the rows
+// after the last group, which follow them.
+__device__ __forceinline__ int64_t count_tiles(const int32_t* offsets, int64_t groups, int64_t m, int bm) {
+  int64_t begin = 0;
+  int n = 0;
+  for (int64_t g0 = 0; g0 < groups; g0 += 64) n += GroupTiles(offsets, groups, m, bm, g0, begin).tiles;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
+  return uniform(n + (m - begin + bm - 1) / bm);
+}
+
+// Tile `tile` of them (group = groups: after the last group; a tile past them
+// all has begin + tile bm >= end).  Every wavefront finds it for itself.
 __device__ __forceinline__ RowRange find_tile(const int32_t* offsets, int64_t groups, int64_t m, int bm,
                                               int64_t tile) {
   const int lane = threadIdx.x % 64;
-  int64_t begin = 0, left = tile;  // of the groups still to come
+  int64_t begin = 0;
+  int left = (int)tile;  // of the groups still to come
   for (int64_t g0 = 0; g0 < groups; g0 += 64) {
-    int64_t end = g0 + lane < groups ? (int64_t)offsets[g0 + lane + 1] : 0;
-    end = end < begin ? begin : end > m ? m : end;
+    const GroupTiles t(offsets, groups, m, bm, g0, begin);
+    int incl = t.tiles;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      const int64_t v = __shfl_up(end, d);
-      if (lane >= d && v > end) end = v;
-    }
-    int64_t start = __shfl_up(end, 1);
-    if (lane == 0) start = begin;
-    const int tiles = (int)((end - start + bm - 1) / bm);
-    int64_t incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int64_t v = __shfl_up(incl, d);
+      const int v = __shfl_up(incl, d);
       if (lane >= d) incl += v;
     }
     const unsigned long long hit = __ballot(left < incl);
@@ -96,15 +123,14 @@ __device__ __forceinline__ RowRange find_tile(const int32_t* offsets, int64_t gr
       const int l = __ffsll((long long)hit) - 1;
       RowRange r;
       r.group = g0 + l;
-      r.begin = uniform(__shfl(start, l));
-      r.end = uniform(__shfl(end, l));
-      r.tile = uniform(left - __shfl(incl - tiles, l));
+      r.begin = uniform(__shfl((int)t.start, l));
+      r.end = uniform(__shfl((int)t.end, l));
+      r.tile = uniform(left - __shfl(incl - t.tiles, l));
       return r;
     }
     left -= __shfl(incl, 63);
-    begin = __shfl(end, 63);
   }
-  return RowRange{groups, uniform(begin), m, uniform(left)};
+  return RowRange{groups, begin, m, uniform(left)};
 }
 
 // Range of group g: the ends as find_tile reads them.
@@ -134,6 +160,7 @@ template <int R, bool KMAJ, int NT>
 struct Loader {
   static constexpr int kN = R * 8 / NT;
   static_assert(kN >= 1 && R * 8 % NT == 0, "whole instructions");
+  static constexpr int kBytes = kN * NT * 16;  // of LDS
   const uint8_t* base;   // first row (KMAJ) or first K row of the range
   int64_t ld_bytes, k_len;
   int64_t rows;          // KMAJ: rows of the tile that exist
@@ -152,8 +179,7 @@ struct Loader {
 #pragma unroll
       for (int i = 0; i < kN; i++) {
         const int s = t + NT * i, row = s / 8, c = (s % 8) ^ (row & 7);
-        const int64_t r = row < rows ? row : rows - 1;
-        voff[i] = (uint32_t)(r * ld_bytes + c * 16);
+        voff[i] = row < rows ? (uint32_t)(row * ld_bytes + c * 16) : 0x7FFFFFF0u;
       }
     } else {
       constexpr int kChunks = R / 8;
@@ -167,37 +193,31 @@ struct Loader {
       }
     }
   }
-  // Loads of step kt.  Elements of K past k_len read as zeros: a buffer load
-  // past its resource's size returns zeros, and the resource ends with the
-  // range's last K row (MN-contiguous), or the lanes past the end of K get an
-  // offset past it (K-contiguous; whole chunks, as the rows are padded to 8).
-  __device__ __forceinline__ void issue(uint8_t* tile, int kt) const {
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
-    const int64_t left = k_len - (int64_t)kt * kStepK;
+  // Resource and lanes of step kt (any kt: steps past the last one load zeros
+  // without touching memory).  Elements of K past k_len read as zeros: a
+  // buffer load past its resource's size returns zeros, and the resource ends
+  // with the range's last K row (MN-contiguous), or the lanes past the end of
+  // K get an offset past it (K-contiguous; whole chunks, as rows are padded to 8).
+  struct Step {
+    __amdgpu_buffer_rsrc_t rsrc;
+    bool off;
+  };
+  __device__ __forceinline__ Step at(int kt) const {
+    const int left = (int)k_len - kt * kStepK;
     if constexpr (KMAJ) {
-      const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(base + (int64_t)kt * (kStepK * 2), rows * ld_bytes);
-      if (left >= kStepK) {
-#pragma unroll
-        for (int i = 0; i < kN; i++)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr_t)(tile + NT * 16 * i + 1024 * wave), 16, (int)voff[i],
-                                                   0, 0, 0);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kN; i++) {
-          const int s = (int)threadIdx.x + NT * i, row = s / 8, c = (s % 8) ^ (row & 7);
-          const uint32_t v = 8 * c < left ? voff[i] : 0x7FFFFFF0u;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr_t)(tile + NT * 16 * i + 1024 * wave), 16, (int)v, 0, 0,
-                                                   0);
-        }
-      }
+      // (the lane's chunk is the same in every instruction: 8 rows per 64 lanes)
+      return Step{make_rsrc(base + (int64_t)kt * (kStepK * 2), left > 0 ? (int)rows * (int)ld_bytes : 0),
+                  8 * (((int)threadIdx.x % 8) ^ ((int)threadIdx.x / 8 & 7)) >= left};
     } else {
-      const int64_t k_rows = left < kStepK ? left : kStepK;
-      const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(base + (int64_t)kt * kStepK * ld_bytes, k_rows * ld_bytes);
-#pragma unroll
-      for (int i = 0; i < kN; i++)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lptr_t)(tile + NT * 16 * i + 1024 * wave), 16, (int)voff[i],
-                                                 0, 0, 0);
+      // (a scalar for the resource: the clamp is a vector instruction)
+      const int k_rows = __builtin_amdgcn_readfirstlane(max(min(left, kStepK), 0));
+      return Step{make_rsrc(base + (int64_t)kt * kStepK * ld_bytes, k_rows * (int)ld_bytes), false};
     }
+  }
+  // Instruction i of a step.
+  __device__ __forceinline__ void issue_one(const Step& s, uint8_t* tile, int wave, int i) const {
+    const uint32_t v = KMAJ && s.off ? 0x7FFFFFF0u : voff[i];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rsrc, (lptr_t)(tile + NT * 16 * i + 1024 * wave), 16, (int)v, 0, 0, 0);
   }
 };
 
@@ -228,14 +248,13 @@ __device__ __forceinline__ void tile_at(int block, int tiles_m, int tiles_n, int
   tn = order_cols ? major : minor;
 }
 
-template <int BM, int BN>
-constexpr int stage_bytes() { return (BM + BN) * kStepK * 2; }
 // One LDS array: a stage of both operands, or half of the rounded C tile
 // (rows padded by 16 bytes).
-template <int BM, int BN>
+template <int BM, int BN, int NT>
 constexpr int lds_array_bytes() {
+  constexpr int stage = Loader<BM, true, NT>::kBytes + Loader<BN, true, NT>::kBytes;
   constexpr int c_half = BM / 2 * (BN + 8) * 2;
-  return stage_bytes<BM, BN>() > c_half ? stage_bytes<BM, BN>() : c_half;
+  return stage > c_half ? stage : c_half;
 }
 
 // Stores the BM x BN tile staged in h0 / h1 to rows [m0, m_end) of C (ld n).
@@ -244,14 +263,24 @@ __device__ __forceinline__ void store_tile(const uint16_t* h0, const uint16_t* h
                                            int64_t m_end, int64_t n0, int64_t n) {
   constexpr int kRow = BN / 8, kPitch = BN + 8;
   static_assert(BM * kRow % NT == 0, "whole turns");
+  auto src_of = [&](int row, int col) {
+    return (row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col;
+  };
   const bool vec = n % 8 == 0;
-#pragma unroll 8
-  for (int it = 0; it < BM * kRow / NT; it++) {
-    const int s = (int)threadIdx.x + it * NT, row = s / kRow, col = (s % kRow) * 8;
-    const uint16_t* src = (row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col;
+  if (vec && m0 + BM <= m_end && n0 + BN <= n) {  // the tile lies inside C: no tests between the stores
+#pragma unroll
+    for (int it = 0; it < BM * kRow / NT; it++) {
+      const int s = (int)threadIdx.x + it * NT, row = s / kRow, col = (s % kRow) * 8;
+      store_out16(c + (m0 + row) * n + n0 + col, *reinterpret_cast<const u32x4*>(src_of(row, col)));
+    }
+    return;
+  }
+  for (int s = threadIdx.x; s < BM * kRow; s += NT) {
+    const int row = s / kRow, col = (s % kRow) * 8;
     const int64_t gr = m0 + row, gc = n0 + col;
     if (gr >= m_end || gc >= n) continue;
     uint16_t* dst = c + gr * n + gc;
+    const uint16_t* src = src_of(row, col);
     if (vec) {
       store_out16(dst, *reinterpret_cast<const u32x4*>(src));
     } else {
@@ -261,22 +290,49 @@ __device__ __forceinline__ void store_tile(const uint16_t* h0, const uint16_t* h
   }
 }
 
+// Four 16-bit values from p of which `left` exist (zeros for the others);
+// quads: the row length is a multiple of 4, so p is 8-byte aligned and the
+// four exist or none.
+__device__ __forceinline__ u32x2 load4(const uint16_t* p, int64_t left, bool quads) {
+  u32x2 v = {0u, 0u};
+  if (quads) {
+    if (left > 0) v = *reinterpret_cast<const u32x2*>(p);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+      if (r < left) v[r / 2] |= (uint32_t)p[r] << (16 * (r & 1));
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ f32x4 widen4(u32x2 v) {
+  return f32x4{dec16<DT>(v[0]), dec16<DT>(v[0] >> 16), dec16<DT>(v[1]), dec16<DT>(v[1] >> 16)};
+}
+
 // Element r of accumulator (i, j) of lane l is C at row 16 i + l % 16 and
 // column 16 j + 4 (l / 16) + r of the wavefront's block (the MFMAs take B's
 // fragment first, so they make C transposed).
-template <int DT, int BM, int BN, int WGM, int WGN, bool AK, bool BK, int GMODE>
+template <int DT, int BM, int BN, int WGM, int WGN, int NS, bool AK, bool BK, int GMODE>
 __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host needs only the symbol to launch)
   constexpr int NT = 64 * WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, FM = WM / 16, FN = WN / 16;
-  __shared__ __attribute__((aligned(1024))) uint8_t s0[lds_array_bytes<BM, BN>()];
-  __shared__ __attribute__((aligned(1024))) uint8_t s1[lds_array_bytes<BM, BN>()];
-  constexpr int kATile = BM * kStepK * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t s0[lds_array_bytes<BM, BN, NT>()];
+  __shared__ __attribute__((aligned(1024))) uint8_t s1[lds_array_bytes<BM, BN, NT>()];
+  __shared__ __attribute__((aligned(1024))) uint8_t s2[NS > 2 ? lds_array_bytes<BM, BN, NT>() : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t s3[NS > 3 ? lds_array_bytes<BM, BN, NT>() : 16];
+  constexpr int kATile = Loader<BM, AK, NT>::kBytes;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, wm = wave / WGN, wn = wave % WGN;
 
   // the tile, its rows of C, its matrices and its range of K
   const int tiles_n = (int)((p.n + BN - 1) / BN);
   int tiles_m = (int)((p.m + BM - 1) / BM);
-  if constexpr (GMODE == BY_ROWS) tiles_m += (int)p.groups;  // each group's last tile may be partial
+  if constexpr (GMODE == BY_ROWS) {
+    // (the grid has room for a partial tile in every group; the tiles there
+    // are are spread over all XCDs)
+    tiles_m = (int)count_tiles(p.offsets, p.groups, p.m, BM);
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+  }
   int tm, tn;
   tile_at((int)blockIdx.x, tiles_m, tiles_n, p.order_cols, p.tile_group, tm, tn);
   const int64_t n0 = (int64_t)tn * BN;
@@ -303,15 +359,15 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     group_range(p.offsets, g, p.k, k0, end);
     k_len = end - k0;
     c_shift = g * p.m * p.n;
-  } else if (BM < 256 && p.splits > 1) {  // (tiles of 256 are not split)
+  } else if (BN < 256 && p.splits > 1) {  // (the wider tiles are not split)
     k0 = (int64_t)blockIdx.y * p.k_part;
     k_len = p.k - k0 < p.k_part ? p.k - k0 : p.k_part;
   }
 
-  Loader<BM, AK, NT> la;
-  Loader<BN, BK, NT> lb;
-  la.init(a, p.lda, m0, m_end, k0, k_len);
-  lb.init(b, p.ldb, n0, p.n, k0, k_len);
+  Loader<BM, AK, NT> da;
+  Loader<BN, BK, NT> db;
+  da.init(a, p.lda, m0, m_end, k0, k_len);
+  db.init(b, p.ldb, n0, p.n, k0, k_len);
   FragReader<2, BM, AK, FM> ra;
   FragReader<2, BN, BK, FN> rb;
   ra.init(wm * WM);
@@ -322,35 +378,109 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
 #pragma unroll
     for (int j = 0; j < FN; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  // Main loop, NS stages, in half steps of 32 of K.  Step kt:
+  //   MFMAs of half 0, the reads of half 1 between them;
+  //   the loads of step kt + 1 have landed; barrier: stage kt is free;
+  //   MFMAs of half 1, between them the loads of step kt + NS into stage kt
+  //   and the reads of half 0 of step kt + 1.
+  // Loads have NS - 1 steps to land and every read nearly a half.  Loads are
+  // issued for steps past the last one too (they move nothing), so that no
+  // step has a branch in it and the count of loads in flight is constant.
+  // The MFMAs go row by row of the wavefront's block, so A's fragment of row i
+  // is read for the next half into its own registers once row i is done; only
+  // B's fragments and A's last one alternate between two sets.  A wavefront
+  // whose rows all lie past the tile's last one only loads.
   const int nk = (int)((k_len + kStepK - 1) / kStepK);
-  auto step = [&](int kt, uint8_t* cur, uint8_t* nxt) {
-    wait_vmcnt<0>();
-    lds_barrier();  // step kt has landed; no wavefront reads stage nxt any more
-    if (kt + 1 < nk) {
-      la.issue(nxt, kt + 1);
-      lb.issue(nxt + kATile, kt + 1);
-    }
+  const int wave_s = __builtin_amdgcn_readfirstlane(wave);
+  constexpr int NA = Loader<BM, AK, NT>::kN, ND = NA + Loader<BN, BK, NT>::kN, NM = FM * FN;
+  u32x4 fa[FM - 1], la0, la1, fb0[FN], fb1[FN];
+  // reads of B: kPerRow after each of rows 1, 2, ..., kGap MFMAs apart
+  constexpr int kPerRow = (FN + FM - 2) / (FM - 1) < 2 ? 2 : (FN + FM - 2) / (FM - 1), kGap = (FN - 1) / kPerRow;
+  static_assert(kGap >= 1 && kPerRow * kGap < FN && kPerRow * (FM - 1) >= FN, "room for B's reads");
+  auto half = [&](const u32x4& last, u32x4& next_last, const u32x4(&fb)[FN], u32x4(&nb)[FN], auto LOAD_, uint8_t* to,
+                  int kt_load, const uint8_t* from, int kk) {
+    constexpr bool LOAD = decltype(LOAD_)::value;
+    const auto sa = da.at(kt_load);
+    const auto sb = db.at(kt_load);
 #pragma unroll
-    for (int kk = 0; kk < 2; kk++) {
-      u32x4 fa[FM], fb[FN];
-      ra.read(cur, kk, fa);
-      rb.read(cur + kATile, kk, fb);
+    for (int i = 0; i < FM; i++) {
 #pragma unroll
-      for (int i = 0; i < FM; i++)
+      for (int j = 0; j < FN; j++) {
+        const int q = i * FN + j;
+        acc[i][j] = mfma16<DT>(fb[j], i < FM - 1 ? fa[i < FM - 1 ? i : 0] : last, acc[i][j]);
+        if (i > 0 && j == 0) fa[i - 1] = ra.read_one(from, kk, i - 1);
+        if (i == 0 && j == FN - 1) next_last = ra.read_one(from, kk, FM - 1);
+        if (i > 0 && j > 0 && j % kGap == 0 && j / kGap <= kPerRow) {
+          const int f = kPerRow * (i - 1) + j / kGap - 1;
+          if (f < FN) nb[f] = rb.read_one(from + kATile, kk, f);
+        }
+        if constexpr (LOAD) {
 #pragma unroll
-        for (int j = 0; j < FN; j++) acc[i][j] = mfma16<DT>(fb[j], fa[i], acc[i][j]);
+          for (int d = 0; d < ND; d++)
+            if (d * NM / ND == q) {
+              if (d < NA) da.issue_one(sa, to, wave_s, d);
+              else db.issue_one(sb, to + kATile, wave_s, d - NA);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
+  auto load_all = [&](uint8_t* to, int kt) {
+    const auto sa = da.at(kt);
+    const auto sb = db.at(kt);
+#pragma unroll
+    for (int i = 0; i < NA; i++) da.issue_one(sa, to, wave_s, i);
+#pragma unroll
+    for (int i = 0; i < ND - NA; i++) db.issue_one(sb, to + kATile, wave_s, i);
+  };
+  auto step = [&](int kt, uint8_t* cur, uint8_t* nxt) {
+    half(la0, la1, fb0, fb1, std::integral_constant<bool, false>(), cur, kt, cur, 1);
+    wait_vmcnt<(NS - 2) * ND>();  // this wavefront's loads of step kt + 1
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    half(la1, la0, fb1, fb0, std::integral_constant<bool, true>(), cur, kt + NS, nxt, 0);
+  };
   if (nk > 0) {
-    la.issue(s0, 0);
-    lb.issue(s0 + kATile, 0);
-  }
-  for (int kt = 0; kt < nk; kt += 2) {
-    step(kt, s0, s1);
-    if (kt + 1 < nk) step(kt + 1, s1, s0);
+    uint8_t* const st[4] = {s0, s1, s2, s3};
+#pragma unroll
+    for (int i = 0; i < NS; i++) load_all(st[i], i);
+    wait_vmcnt<(NS - 1) * ND>();
+    lds_barrier();
+    if (GMODE == BY_ROWS && m0 + (int64_t)(wave_s / WGN) * WM >= m_end) {
+      const int steps = NS == 2 ? nk + nk % 2 : nk;  // as many barriers as the others
+      for (int kt = 0; kt < steps; kt += NS) {
+#pragma unroll
+        for (int i = 0; i < NS; i++) {
+          if (kt + i >= steps) break;
+          wait_vmcnt<(NS - 2) * ND>();
+          lds_barrier();
+          load_all(st[i], kt + i + NS);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < FM - 1; i++) fa[i] = ra.read_one(s0, 0, i);
+      la0 = ra.read_one(s0, 0, FM - 1);
+      rb.read(s0 + kATile, 0, fb0);
+      // two stages: an odd last step is followed by one of zeros (a copy of
+      // the step for it costs registers in the loop)
+      constexpr int kOver = NS == 2 ? 1 : 0;
+      int kt = 0;
+      for (; kt + NS <= nk + kOver; kt += NS) {
+#pragma unroll
+        for (int i = 0; i < NS; i++) step(kt + i, st[i], st[(i + 1) % NS]);
+      }
+      if constexpr (NS > 2) {
+#pragma unroll
+        for (int i = 0; i < NS - 1; i++)
+          if (kt + i < nk) step(kt + i, st[i], st[i + 1]);
+      }
+    }
+    wait_vmcnt<0>();  // the last loads' zeros are in LDS before the epilogue's values
   }
 
-  if constexpr (GMODE == DENSE && BM < 256) {
+  if constexpr (GMODE == DENSE && BN < 256) {
     if (p.splits > 1) {  // fp32 sums, tiles whole
       const int64_t ld = (int64_t)tiles_n * BN;
       float* part = p.partial + ((int64_t)blockIdx.y * tiles_m * BM + m0 + wm * WM + lane % 16) * ld + n0 + wn * WN +
@@ -371,13 +501,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     const int row = wm * WM + 16 * i + lane % 16, col = wn * WN + 16 * j + 4 * (lane / 16);
     return reinterpret_cast<u32x2*>((row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col);
   };
+  const bool quads = p.n % 4 == 0;
+  const int64_t col0 = n0 + wn * WN + 4 * (lane / 16);  // this lane's first column
   if (bias) {
 #pragma unroll
     for (int j = 0; j < FN; j++) {
-      const int64_t col = n0 + wn * WN + 16 * j + 4 * (lane / 16);
-      float bv[4];
-#pragma unroll
-      for (int r = 0; r < 4; r++) bv[r] = col + r < p.n ? dec16<DT>(bias[col + r]) : 0.0f;
+      const f32x4 bv = widen4<DT>(load4(bias + col0 + 16 * j, p.n - col0 - 16 * j, quads));
 #pragma unroll
       for (int i = 0; i < FM; i++)
 #pragma unroll
@@ -401,16 +530,21 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
 #pragma unroll
     for (int i = 0; i < FM; i++) {
       const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
+      u32x2 rv[FN];
+      if (residual) {
+#pragma unroll
+        for (int j = 0; j < FN; j++)
+          rv[j] = load4(residual + row * p.n + col0 + 16 * j, row < m_end ? p.n - col0 - 16 * j : 0, quads);
+      }
 #pragma unroll
       for (int j = 0; j < FN; j++) {
         f32x4 v = acc[i][j];
 #pragma unroll
         for (int r = 0; r < 4; r++) v[r] = act_of<ACT>(v[r]);
-        if (residual && row < m_end) {
-          const int64_t col = n0 + wn * WN + 16 * j + 4 * (lane / 16);
+        if (residual) {
+          const f32x4 f = widen4<DT>(rv[j]);
 #pragma unroll
-          for (int r = 0; r < 4; r++)
-            if (col + r < p.n) v[r] += dec16<DT>(residual[row * p.n + col + r]);
+          for (int r = 0; r < 4; r++) v[r] += f[r];
         }
         *staged(i, j) = u32x2{pack2_16<DT>(v[0], v[1]), pack2_16<DT>(v[2], v[3])};
       }
@@ -418,6 +552,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
   });
   __syncthreads();
   store_tile<BM, BN, NT>(h0, h1, static_cast<uint16_t*>(p.out) + c_shift, m0, m_end, n0, p.n);
+#endif
 }
 
 }  // namespace lin

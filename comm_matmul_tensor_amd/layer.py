@@ -10,7 +10,6 @@ kernels have read it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -60,8 +59,9 @@ def _like(t, name: str, shape, dtype):
     """An optional argument's shape and dtype (the C ABI sees only pointers and sizes)."""
     if t is None:
         return
-    _tensor(t, name)
-    if tuple(t.shape) != tuple(shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -73,55 +73,60 @@ def _needed(t, name: str, shape, dtype):
     _like(t, name, shape, dtype)
 
 
-class _Call:
-    """Where a call runs: the tensors' device, which must be the current one, and the stream."""
+def _place(names: str, *tensors) -> int:
+    """The current stream's handle, after checking that every tensor is contiguous and on the
+    current device (a decoding step's calls are short, so the checks are kept few and cheap)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError(f"{_name(names, t, tensors)} must be contiguous")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError(f"{_name(names, t, tensors)} must be a device tensor")
+            if dev is not None:
+                raise ValueError(f"{_name(names, t, tensors)} is on {t.device}, the other tensors on cuda:{dev}")
+            dev = d
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev} but the current device is cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev)
 
-    def __init__(self, stream, **named):
-        dev = None
-        for name, t in named.items():
-            if t is None:
-                continue
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a device tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-        current = torch.cuda.current_device()
-        if dev.index != current:
-            raise ValueError(f"tensors are on {dev} but the current device is cuda:{current}")
-        self.device = dev
-        now = torch.cuda.current_stream()
-        if stream is None:
-            self.handle, self.scope = now.cuda_stream, contextlib.nullcontext()
-            return
-        st = _stream_obj(stream)
-        self.handle, self.scope = st.cuda_stream, torch.cuda.stream(st)
-        if st.cuda_stream != now.cuda_stream:
-            for t in named.values():
-                if t is not None:
-                    t.record_stream(st)
 
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+# the handle alone, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def workspace(self, given, size_fn: str, *sizes):
-        """The workspace tensor of a call (None where it needs none)."""
-        n = ctypes.c_size_t(0)
-        _check(getattr(_lib, size_fn)(*sizes, ctypes.byref(n)))
-        if given is not None:
-            return given
-        return self.empty((n.value,), torch.uint8) if n.value else None
+
+def _name(names: str, t, tensors) -> str:
+    return names.split()[next(i for i, u in enumerate(tensors) if u is t)]
+
+
+def _on(stream, fn, *args, **kwargs):
+    """fn on another stream: its tensors are recorded there, and what it allocates is allocated there."""
+    st = _stream_obj(stream)
+    if st.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        for t in (*args, *kwargs.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(st)
+    with torch.cuda.stream(st):
+        return fn(*args, **kwargs)
+
+
+def _workspace(given, like, size_fn, *sizes):
+    """(tensor, pointer, bytes) of a call's workspace; nothing where it needs none."""
+    if given is not None:
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    n = ctypes.c_size_t(0)
+    _check(size_fn(*sizes, ctypes.byref(n)))
+    if n.value == 0:
+        return None, None, 0
+    t = like.new_empty((n.value,), dtype=torch.uint8)
+    return t, t.data_ptr(), n.value
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
-
-
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _workspace_ok(t):
@@ -143,6 +148,9 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[t
     None for the 16-bit output.  sum is s in x's dtype: x itself without a residual.  rstd (rows)
     fp32 comes with need_rstd, for mc2_add_rms_norm_grad.
     """
+    if stream is not None:
+        return _on(stream, mc2_add_rms_norm, x, weight, residual, eps=eps, out_dtype=out_dtype, group=group,
+                   need_rstd=need_rstd, out=out, scale_out=scale_out, sum_out=sum_out, rstd_out=rstd_out)
     shape = _tensor(x, "x")
     if len(shape) < 1:
         raise ValueError("x must have a last dimension")
@@ -151,8 +159,10 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[t
     _half(x, "x")
     dt = x.dtype
     if out is not None:
-        out_dtype = _tensor(out, "out") and out.dtype
-    out_dtype = out_dtype or dt
+        _tensor(out, "out")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = dt
     eight = out_dtype in (torch.int8, torch.float8_e4m3fn)
     if not eight and out_dtype != dt:
         raise TypeError(f"out_dtype must be {dt}, int8 or float8_e4m3fn, got {out_dtype}")
@@ -167,20 +177,19 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[t
     if scale_out is not None and not eight:
         raise ValueError("scale_out goes with an 8-bit output")
     _like(scale_out, "scale_out", scales, torch.float32)
-    call = _Call(stream, x=x, weight=weight, residual=residual, out=out, scale_out=scale_out, sum_out=sum_out,
-                 rstd_out=rstd_out)
-    with call.scope:
-        if out is None:
-            out = call.empty(shape, out_dtype)
-        if eight and scale_out is None:
-            scale_out = call.empty(scales, torch.float32)
-        if residual is not None and sum_out is None:
-            sum_out = call.empty(shape, dt)
-        if need_rstd and rstd_out is None:
-            rstd_out = call.empty((rows,), torch.float32)
-        _check(_lib.mc2_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, h, _TORCH_DT[dt], eps,
-                                     out.data_ptr(), _TORCH_DT[out_dtype], _ptr(scale_out), group, _ptr(sum_out),
-                                     _ptr(rstd_out), call.handle))
+    handle = _place("x weight residual out scale_out sum_out rstd_out", x, weight, residual, out, scale_out, sum_out,
+                    rstd_out)
+    if out is None:
+        out = torch.empty_like(x) if not eight else x.new_empty(shape, dtype=out_dtype)
+    if eight and scale_out is None:
+        scale_out = x.new_empty(scales, dtype=torch.float32)
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty_like(x)
+    if need_rstd and rstd_out is None:
+        rstd_out = x.new_empty((rows,), dtype=torch.float32)
+    _check(_lib.mc2_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, h, _TORCH_DT[dt], eps,
+                                 out.data_ptr(), _TORCH_DT[out_dtype], _ptr(scale_out), group, _ptr(sum_out),
+                                 _ptr(rstd_out), handle))
     return out, scale_out, x if sum_out is None else sum_out, rstd_out
 
 
@@ -190,6 +199,9 @@ def mc2_add_rms_norm_grad(dout: torch.Tensor, s: torch.Tensor, weight: torch.Ten
                           stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(dx, dweight) of mc2_add_rms_norm's 16-bit output; s and rstd are its sum and rstd, dsum the
     gradient that reached sum.  dx is the gradient of x and of residual."""
+    if stream is not None:
+        return _on(stream, mc2_add_rms_norm_grad, dout, s, weight, rstd, dsum, dx=dx, dweight=dweight,
+                   workspace=workspace)
     shape = _tensor(s, "s")
     if len(shape) < 1:
         raise ValueError("s must have a last dimension")
@@ -204,17 +216,14 @@ def mc2_add_rms_norm_grad(dout: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     _like(dx, "dx", shape, dt)
     _like(dweight, "dweight", (h,), dt)
     _workspace_ok(workspace)
-    call = _Call(stream, dout=dout, s=s, weight=weight, rstd=rstd, dsum=dsum, dx=dx, dweight=dweight,
-                 workspace=workspace)
-    with call.scope:
-        workspace = call.workspace(workspace, "mc2_add_rms_norm_grad_workspace_size", rows, h)
-        if dx is None:
-            dx = call.empty(shape, dt)
-        if dweight is None:
-            dweight = call.empty((h,), dt)
-        _check(_lib.mc2_add_rms_norm_grad(dout.data_ptr(), _ptr(dsum), s.data_ptr(), weight.data_ptr(),
-                                          rstd.data_ptr(), rows, h, _TORCH_DT[dt], dx.data_ptr(), dweight.data_ptr(),
-                                          _ptr(workspace), _bytes(workspace), call.handle))
+    handle = _place("dout s weight rstd dsum dx dweight workspace", dout, s, weight, rstd, dsum, dx, dweight, workspace)
+    _ws, ws, ws_bytes = _workspace(workspace, s, _lib.mc2_add_rms_norm_grad_workspace_size, rows, h)
+    if dx is None:
+        dx = torch.empty_like(s)
+    if dweight is None:
+        dweight = torch.empty_like(weight)
+    _check(_lib.mc2_add_rms_norm_grad(dout.data_ptr(), _ptr(dsum), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+                                      rows, h, _TORCH_DT[dt], dx.data_ptr(), dweight.data_ptr(), ws, ws_bytes, handle))
     return dx, dweight
 
 
@@ -247,6 +256,9 @@ def mc2_linear_act(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     (G + 1 int32 on the device) w is (G, n, k), bias (G, n), and rows group_offsets[g] ..
     group_offsets[g + 1] use matrix g; rows after the last range get z = 0.
     """
+    if stream is not None:
+        return _on(stream, mc2_linear_act, x, w, bias, residual, act=act, group_offsets=group_offsets, need_z=need_z,
+                   out=out, z_out=z_out, workspace=workspace)
     m, k, n, groups = _linear_sizes(x, w, group_offsets)
     dt = x.dtype
     _like(bias, "bias", (groups, n) if groups else (n,), dt)
@@ -254,17 +266,15 @@ def mc2_linear_act(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     _like(out, "out", (m, n), dt)
     _like(z_out, "z_out", (m, n), dt)
     _workspace_ok(workspace)
-    call = _Call(stream, x=x, w=w, bias=bias, residual=residual, group_offsets=group_offsets, out=out, z_out=z_out,
-                 workspace=workspace)
-    with call.scope:
-        workspace = call.workspace(workspace, "mc2_linear_act_workspace_size", m, k, n, groups)
-        if out is None:
-            out = call.empty((m, n), dt)
-        if need_z and z_out is None:
-            z_out = call.empty((m, n), dt)
-        _check(_lib.mc2_linear_act(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), m, k, n,
-                                   _ptr(group_offsets), groups, _TORCH_DT[dt], act, out.data_ptr(), _ptr(z_out),
-                                   _ptr(workspace), _bytes(workspace), call.handle))
+    handle = _place("x w bias residual group_offsets out z_out workspace", x, w, bias, residual, group_offsets, out,
+                    z_out, workspace)
+    _ws, ws, ws_bytes = _workspace(workspace, x, _lib.mc2_linear_act_workspace_size, m, k, n, groups)
+    if out is None:
+        out = x.new_empty((m, n))
+    if need_z and z_out is None:
+        z_out = x.new_empty((m, n))
+    _check(_lib.mc2_linear_act(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), m, k, n, _ptr(group_offsets),
+                               groups, _TORCH_DT[dt], act, out.data_ptr(), _ptr(z_out), ws, ws_bytes, handle))
     return out, z_out
 
 
@@ -276,6 +286,9 @@ def mc2_linear_act_grad(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z:
                         ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
     """(dx, dw, dbias) of mc2_linear_act, each None unless wanted (need_*, or given); z is its
     pre-activation (not needed with MC2_ACT_NONE).  The residual's gradient is dout itself."""
+    if stream is not None:
+        return _on(stream, mc2_linear_act_grad, dout, x, w, z, act=act, group_offsets=group_offsets, need_dx=need_dx,
+                   need_dw=need_dw, need_dbias=need_dbias, dx=dx, dw=dw, dbias=dbias, workspace=workspace)
     m, k, n, groups = _linear_sizes(x, w, group_offsets)
     dt = x.dtype
     bias_shape = (groups, n) if groups else (n,)
@@ -288,19 +301,17 @@ def mc2_linear_act_grad(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z:
     _like(dw, "dw", w.shape, dt)
     _like(dbias, "dbias", bias_shape, dt)
     _workspace_ok(workspace)
-    call = _Call(stream, dout=dout, x=x, w=w, z=z, group_offsets=group_offsets, dx=dx, dw=dw, dbias=dbias,
-                 workspace=workspace)
-    with call.scope:
-        workspace = call.workspace(workspace, "mc2_linear_act_grad_workspace_size", m, k, n, groups)
-        if need_dx and dx is None:
-            dx = call.empty((m, k), dt)
-        if need_dw and dw is None:
-            dw = call.empty(w.shape, dt)
-        if need_dbias and dbias is None:
-            dbias = call.empty(bias_shape, dt)
-        _check(_lib.mc2_linear_act_grad(dout.data_ptr(), _ptr(z), x.data_ptr(), w.data_ptr(), m, k, n,
-                                        _ptr(group_offsets), groups, _TORCH_DT[dt], act, _ptr(dx), _ptr(dw),
-                                        _ptr(dbias), _ptr(workspace), _bytes(workspace), call.handle))
+    handle = _place("dout x w z group_offsets dx dw dbias workspace", dout, x, w, z, group_offsets, dx, dw, dbias,
+                    workspace)
+    _ws, ws, ws_bytes = _workspace(workspace, x, _lib.mc2_linear_act_grad_workspace_size, m, k, n, groups)
+    if need_dx and dx is None:
+        dx = torch.empty_like(x)
+    if need_dw and dw is None:
+        dw = torch.empty_like(w)
+    if need_dbias and dbias is None:
+        dbias = x.new_empty(bias_shape)
+    _check(_lib.mc2_linear_act_grad(dout.data_ptr(), _ptr(z), x.data_ptr(), w.data_ptr(), m, k, n, _ptr(group_offsets),
+                                    groups, _TORCH_DT[dt], act, _ptr(dx), _ptr(dw), _ptr(dbias), ws, ws_bytes, handle))
     return dx, dw, dbias
 
 
@@ -312,6 +323,9 @@ def mc2_moe_permute(x: torch.Tensor, expert_ids: torch.Tensor, experts: int, *, 
     """Rows of x (tokens, h) for every choice expert_ids[t][j] (int32), sorted by expert and then by
     t * top + j: returns (out (tokens * top, h), row_map (tokens, top) int32, offsets (experts + 1)
     int32).  Ids outside [0, experts) are dropped: row_map -1; out's last rows are then 0."""
+    if stream is not None:
+        return _on(stream, mc2_moe_permute, x, expert_ids, experts, out=out, row_map=row_map, offsets=offsets,
+                   workspace=workspace)
     tokens, h = _tensor(x, "x", 2)
     _half(x, "x")
     top = _tensor(expert_ids, "expert_ids", 2)[1]
@@ -320,18 +334,16 @@ def mc2_moe_permute(x: torch.Tensor, expert_ids: torch.Tensor, experts: int, *, 
     _like(row_map, "row_map", (tokens, top), torch.int32)
     _like(offsets, "offsets", (experts + 1,), torch.int32)
     _workspace_ok(workspace)
-    call = _Call(stream, x=x, expert_ids=expert_ids, out=out, row_map=row_map, offsets=offsets, workspace=workspace)
-    with call.scope:
-        workspace = call.workspace(workspace, "mc2_moe_permute_workspace_size", tokens, top, experts)
-        if out is None:
-            out = call.empty((tokens * top, h), x.dtype)
-        if row_map is None:
-            row_map = call.empty((tokens, top), torch.int32)
-        if offsets is None:
-            offsets = call.empty((experts + 1,), torch.int32)
-        _check(_lib.mc2_moe_permute(x.data_ptr(), expert_ids.data_ptr(), tokens, top, h, experts, _TORCH_DT[x.dtype],
-                                    out.data_ptr(), row_map.data_ptr(), offsets.data_ptr(), _ptr(workspace),
-                                    _bytes(workspace), call.handle))
+    handle = _place("x expert_ids out row_map offsets workspace", x, expert_ids, out, row_map, offsets, workspace)
+    _ws, ws, ws_bytes = _workspace(workspace, x, _lib.mc2_moe_permute_workspace_size, tokens, top, experts)
+    if out is None:
+        out = x.new_empty((tokens * top, h))
+    if row_map is None:
+        row_map = torch.empty_like(expert_ids)
+    if offsets is None:
+        offsets = expert_ids.new_empty((experts + 1,))
+    _check(_lib.mc2_moe_permute(x.data_ptr(), expert_ids.data_ptr(), tokens, top, h, experts, _TORCH_DT[x.dtype],
+                                out.data_ptr(), row_map.data_ptr(), offsets.data_ptr(), ws, ws_bytes, handle))
     return out, row_map, offsets
 
 
@@ -339,18 +351,19 @@ def mc2_moe_unpermute(y: torch.Tensor, row_map: torch.Tensor, weights: Optional[
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out[t] = sum over j of weights[t][j] * y[row_map[t][j]] (weights (tokens, top) fp32, or None
     for 1).  Without weights it is also mc2_moe_permute's gradient."""
+    if stream is not None:
+        return _on(stream, mc2_moe_unpermute, y, row_map, weights, out=out)
     rows, h = _tensor(y, "y", 2)
     _half(y, "y")
     tokens, top = _tensor(row_map, "row_map", 2)
     _needed(row_map, "row_map", (tokens, top), torch.int32)
     _like(weights, "weights", (tokens, top), torch.float32)
     _like(out, "out", (tokens, h), y.dtype)
-    call = _Call(stream, y=y, row_map=row_map, weights=weights, out=out)
-    with call.scope:
-        if out is None:
-            out = call.empty((tokens, h), y.dtype)
-        _check(_lib.mc2_moe_unpermute(y.data_ptr(), row_map.data_ptr(), _ptr(weights), tokens, top, h, rows,
-                                      _TORCH_DT[y.dtype], out.data_ptr(), call.handle))
+    handle = _place("y row_map weights out", y, row_map, weights, out)
+    if out is None:
+        out = y.new_empty((tokens, h))
+    _check(_lib.mc2_moe_unpermute(y.data_ptr(), row_map.data_ptr(), _ptr(weights), tokens, top, h, rows,
+                                  _TORCH_DT[y.dtype], out.data_ptr(), handle))
     return out
 
 
@@ -359,6 +372,9 @@ def mc2_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_map: torch.T
                            dy: Optional[torch.Tensor] = None, dweights: Optional[torch.Tensor] = None, stream=None
                            ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """(dy, dweights) of mc2_moe_unpermute for a row_map that mc2_moe_permute gave."""
+    if stream is not None:
+        return _on(stream, mc2_moe_unpermute_grad, dout, y, row_map, weights, need_dweights=need_dweights, dy=dy,
+                   dweights=dweights)
     rows, h = _tensor(y, "y", 2)
     _half(y, "y")
     tokens, top = _tensor(row_map, "row_map", 2)
@@ -367,15 +383,13 @@ def mc2_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_map: torch.T
     _like(weights, "weights", (tokens, top), torch.float32)
     _like(dy, "dy", (rows, h), y.dtype)
     _like(dweights, "dweights", (tokens, top), torch.float32)
-    call = _Call(stream, dout=dout, y=y, row_map=row_map, weights=weights, dy=dy, dweights=dweights)
-    with call.scope:
-        if dy is None:
-            dy = call.empty((rows, h), y.dtype)
-        if need_dweights and dweights is None:
-            dweights = call.empty((tokens, top), torch.float32)
-        _check(_lib.mc2_moe_unpermute_grad(dout.data_ptr(), y.data_ptr(), row_map.data_ptr(), _ptr(weights), tokens,
-                                           top, h, rows, _TORCH_DT[y.dtype], dy.data_ptr(), _ptr(dweights),
-                                           call.handle))
+    handle = _place("dout y row_map weights dy dweights", dout, y, row_map, weights, dy, dweights)
+    if dy is None:
+        dy = torch.empty_like(y)
+    if need_dweights and dweights is None:
+        dweights = y.new_empty((tokens, top), dtype=torch.float32)
+    _check(_lib.mc2_moe_unpermute_grad(dout.data_ptr(), y.data_ptr(), row_map.data_ptr(), _ptr(weights), tokens, top,
+                                       h, rows, _TORCH_DT[y.dtype], dy.data_ptr(), _ptr(dweights), handle))
     return dy, dweights
 
 
