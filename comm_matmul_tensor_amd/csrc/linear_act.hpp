@@ -60,8 +60,9 @@ __device__ __forceinline__ float act_slope(float z) {
     return __builtin_fmaf(z * 0.39894228040143267794f, e, p);
   }
   if constexpr (ACT == ACT_GELU_TANH) {
-    const float p = sigmoid(z * __builtin_fmaf(kTanhB, z * z, kTanhA));
-    return __builtin_fmaf(z * p * (1.0f - p), __builtin_fmaf(3.0f * kTanhB, z * z, kTanhA), p);
+    // (z^2 kept finite: its product with the 0 of 1 - p is 0)
+    const float z2 = fminf(z * z, 1e30f), p = sigmoid(z * __builtin_fmaf(kTanhB, z2, kTanhA));
+    return __builtin_fmaf(z * p * (1.0f - p), __builtin_fmaf(3.0f * kTanhB, z2, kTanhA), p);
   }
   if constexpr (ACT == ACT_SILU) {
     const float p = sigmoid(z);

@@ -22,6 +22,11 @@ namespace mc2 {
 namespace {
 
 constexpr int kChunk = 8192;   // choices per workgroup of the sort
+// Workgroups that walk the tokens of the gradient: enough to fill the CUs
+// once.  More in flight only scatter the rows read and written at a time:
+// 8192 tokens, 4 choices, h = 4096: 1024 workgroups 125 us, 2048 130, 4096
+// 139, one per token 142; 256 are too few (181).
+constexpr int kGradBlocks = 1024;
 constexpr int kZeroBlocks = 64;  // workgroups that clear the rows of no choice
 
 __device__ __forceinline__ int expert_of(const int32_t* ids, int64_t i, int64_t end, int experts) {
@@ -293,64 +298,65 @@ __global__ __launch_bounds__(256) void unpermute_grad(UnpermuteArgs a, int64_t t
                    kZeroBlocks);
     return;
   }
-  const int64_t t = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR;
-  if (t >= a.tokens) return;  // only with TPR < 256, which has no barrier
   const int lane = threadIdx.x % TPR;
-  const int32_t* map = a.row_map + t * a.top;
-  const uint16_t* dout = static_cast<const uint16_t*>(a.dout) + t * h;
   const uint16_t* y = static_cast<const uint16_t*>(a.y);
   int turn = 0;
-  for (int64_t j0 = 0; j0 < a.top; j0 += JB, turn ^= 1) {
-    int64_t r[JB];
-    float w[JB], dot[JB];
-#pragma unroll
-    for (int j = 0; j < JB; j++) {
-      r[j] = j0 + j < a.top ? map[j0 + j] : -1;
-      if (r[j] >= a.rows) r[j] = -1;
-      w[j] = r[j] >= 0 ? (a.weights ? a.weights[t * a.top + j0 + j] : 1.0f) : 0.0f;
-      dot[j] = 0.0f;
-    }
-    for (int64_t c = 8 * lane; c < h; c += 8 * TPR) {
-      const u32x4 vd = load_chunk<VEC>(dout, c, h);
-      u32x4 vy[JB];
+  const int64_t step = token_blocks * (256 / TPR);
+  for (int64_t t = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR; t < a.tokens; t += step) {
+    const int32_t* map = a.row_map + t * a.top;
+    const uint16_t* dout = static_cast<const uint16_t*>(a.dout) + t * h;
+    for (int64_t j0 = 0; j0 < a.top; j0 += JB, turn ^= 1) {
+      int64_t r[JB];
+      float w[JB], dot[JB];
 #pragma unroll
       for (int j = 0; j < JB; j++) {
-        vy[j] = u32x4{0u, 0u, 0u, 0u};
-        if (a.dweights && r[j] >= 0) vy[j] = load_chunk<VEC>(y + r[j] * h, c, h);
+        r[j] = j0 + j < a.top ? map[j0 + j] : -1;
+        if (r[j] >= a.rows) r[j] = -1;
+        w[j] = r[j] >= 0 ? (a.weights ? a.weights[t * a.top + j0 + j] : 1.0f) : 0.0f;
+        dot[j] = 0.0f;
       }
-      float d[8];
-      unpack8<DT>(vd, d);
-#pragma unroll
-      for (int j = 0; j < JB; j++) {
-        float f[8], g[8];
-        unpack8<DT>(vy[j], f);
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-          dot[j] = __builtin_fmaf(f[e], d[e], dot[j]);
-          g[e] = w[j] * d[e];
-        }
-        if (dy && r[j] >= 0) store_chunk<VEC, true>(dy + r[j] * h, c, h, pack8<DT>(g));
-      }
-    }
-    if (a.dweights) {
-#pragma unroll
-      for (int j = 0; j < JB; j++) {
-        dot[j] = wave_sum(dot[j]);
-        if (WAVES > 1 && threadIdx.x % 64 == 0) red[turn][j][threadIdx.x / 64] = dot[j];
-      }
-      if constexpr (WAVES > 1) {
-        __syncthreads();
+      for (int64_t c = 8 * lane; c < h; c += 8 * TPR) {
+        const u32x4 vd = load_chunk<VEC>(dout, c, h);
+        u32x4 vy[JB];
 #pragma unroll
         for (int j = 0; j < JB; j++) {
-          dot[j] = red[turn][j][0];
+          vy[j] = u32x4{0u, 0u, 0u, 0u};
+          if (a.dweights && r[j] >= 0) vy[j] = load_chunk<VEC>(y + r[j] * h, c, h);
+        }
+        float d[8];
+        unpack8<DT>(vd, d);
 #pragma unroll
-          for (int v = 1; v < WAVES; v++) dot[j] += red[turn][j][v];
+        for (int j = 0; j < JB; j++) {
+          float f[8], g[8];
+          unpack8<DT>(vy[j], f);
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            dot[j] = __builtin_fmaf(f[e], d[e], dot[j]);
+            g[e] = w[j] * d[e];
+          }
+          if (dy && r[j] >= 0) store_chunk<VEC, true>(dy + r[j] * h, c, h, pack8<DT>(g));
         }
       }
-      if (lane == 0) {
+      if (a.dweights) {
 #pragma unroll
-        for (int j = 0; j < JB; j++)
-          if (j0 + j < a.top) a.dweights[t * a.top + j0 + j] = r[j] >= 0 ? dot[j] : 0.0f;
+        for (int j = 0; j < JB; j++) {
+          dot[j] = wave_sum(dot[j]);
+          if (WAVES > 1 && threadIdx.x % 64 == 0) red[turn][j][threadIdx.x / 64] = dot[j];
+        }
+        if constexpr (WAVES > 1) {
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < JB; j++) {
+            dot[j] = red[turn][j][0];
+#pragma unroll
+            for (int v = 1; v < WAVES; v++) dot[j] += red[turn][j][v];
+          }
+        }
+        if (lane == 0) {
+#pragma unroll
+          for (int j = 0; j < JB; j++)
+            if (j0 + j < a.top) a.dweights[t * a.top + j0 + j] = r[j] >= 0 ? dot[j] : 0.0f;
+        }
       }
     }
   }
@@ -370,7 +376,7 @@ hipError_t unpermute_launch(const UnpermuteArgs& a, hipStream_t s) {
 
 template <int DT, bool VEC, int TPR>
 hipError_t unpermute_grad_launch(const UnpermuteArgs& a, hipStream_t s) {
-  const int64_t blocks = (a.tokens + 256 / TPR - 1) / (256 / TPR);
+  const int64_t blocks = std::min<int64_t>((a.tokens + 256 / TPR - 1) / (256 / TPR), kGradBlocks);
   const unsigned grid = (unsigned)(blocks + kZeroBlocks);
   if (a.top == 1) unpermute_grad<DT, VEC, TPR, 1><<<grid, 256, 0, s>>>(a, blocks);
   else if (a.top == 2) unpermute_grad<DT, VEC, TPR, 2><<<grid, 256, 0, s>>>(a, blocks);

@@ -76,12 +76,12 @@ def _needed(t, name: str, shape, dtype):
 def _place(names: str, *tensors) -> int:
     """The current stream's handle, after checking that every tensor is contiguous and on the
     current device (a decoding step's calls are short, so the checks are kept few and cheap)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
+    given = [t for t in tensors if t is not None]
+    for t in given:
         if not t.is_contiguous():
             raise ValueError(f"{_name(names, t, tensors)} must be contiguous")
+    dev = None
+    for t in given:
         d = t.get_device()
         if d != dev:
             if d < 0:
