@@ -65,7 +65,7 @@ hipError_t launch_pad_rows(const void* src, int64_t rows, int64_t k, void* dst, 
 // and their sums are added in wavefront order.  An MFMA takes 16 rows of w
 // (its first operand) and 16 rows of x (rows past m repeat the last one and
 // are not stored); fragments come straight from memory, U of each in flight.
-constexpr int kSkinnyU = 8;
+constexpr int kSkinnyU = 4;
 template <int DT, int MF, int WAVES, bool VEC>
 __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(Product p) {
   __shared__ float red[WAVES][MF * 256];
@@ -124,9 +124,11 @@ template <int DT, int MF>
 hipError_t launch_skinny(const Product& p, hipStream_t s) {
   const unsigned blocks = (unsigned)((p.n + 15) / 16);
   const bool vec = p.k % 8 == 0;
-  // enough wavefronts in flight to cover HBM's latency: 4 a workgroup where
-  // the columns make 256 workgroups, else 16
-  if (blocks >= 256) {
+  // 4 wavefronts a workgroup where the columns make 1.5 to 4 workgroups per
+  // CU, 16 where they make fewer (to cover HBM's latency) or more (fewer rows
+  // of w read at a time).  One row, us with 4 / 16: 4096 x 7168 12.7 / 13.4,
+  // 7168 x 4096 14.2 / 11.5, 8192 x 28672 92 / 84 (470 MB, 5.6 TB/s).
+  if (blocks >= 384 && blocks < 1024) {
     if (vec) skinny_kernel<DT, MF, 4, true><<<blocks, 256, 0, s>>>(p);
     else skinny_kernel<DT, MF, 4, false><<<blocks, 256, 0, s>>>(p);
   } else {
@@ -137,11 +139,14 @@ hipError_t launch_skinny(const Product& p, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- dz and bias sums
-// dz = dout act'(z) for a tile of 64 rows (of one group) x 256 columns, and
-// the column sums of the unrounded dz over the tile's rows: thread (r, c) of
-// 8 x 32 takes rows r, r + 8, ... and 8 columns; the 8 rows' sums are added
-// in order.
-constexpr int kDzRows = 64, kDzCols = 256;
+// dz = dout act'(z) for a tile of 64 rows (of one group), and the column sums
+// of the unrounded dz over the tile's rows.  A row of the tile is taken by tpr
+// threads with 8 columns each (fewer than kDzThreads where n is small), and
+// the sums of the 256 / tpr rows in flight are added in order.  Bound by HBM
+// and, with gelu, nearly as much by its arithmetic: 4096 x 7168 32 us for the
+// sums alone, 38 with dz stored.  Wider tiles (a row's 4 KB at a time) or more
+// rows in flight per thread took 35 to 55: they leave fewer wavefronts.
+constexpr int kDzRows = 64, kDzThreads = 32;  // rows of a tile, most threads of a row
 struct DzArgs {
   const uint16_t *dout, *z;
   uint16_t* dz;    // (m, ld) or NULL
@@ -149,10 +154,11 @@ struct DzArgs {
   int64_t m, n, ld;
   const int32_t* offsets;
   int64_t groups;
+  int tpr;
 };
 template <int DT, int ACT, bool VEC>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-  __shared__ float red[8][kDzCols + 8];
+  __shared__ float red[256 * 8];  // [row of threads][column]
   int64_t m0 = (int64_t)blockIdx.x * kDzRows, m_end = a.m;
   if (a.groups > 0) {
     const RowRange r = find_tile(a.offsets, a.groups, a.m, kDzRows, blockIdx.x);
@@ -161,12 +167,12 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
     m_end = r.end;
   }
   if (m0 + kDzRows < m_end) m_end = m0 + kDzRows;
-  const int rt = threadIdx.x / 32, ct = threadIdx.x % 32;
-  const int64_t c = (int64_t)blockIdx.y * kDzCols + 8 * ct;
+  const int tpr = a.tpr, rows = 256 / tpr, rt = threadIdx.x / tpr, ct = threadIdx.x % tpr;
+  const int64_t c0 = (int64_t)blockIdx.y * tpr * 8, c = c0 + 8 * ct;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < a.n) {
-#pragma unroll 4
-    for (int64_t row = m0 + rt; row < m_end; row += 8) {
+#pragma unroll 2
+    for (int64_t row = m0 + rt; row < m_end; row += rows) {
       float d[8];
       unpack8<DT>(load_chunk<VEC>(a.dout + row * a.n, c, a.n), d);
       if constexpr (ACT != ACT_NONE) {
@@ -185,14 +191,13 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   }
   if (!a.partial) return;
 #pragma unroll
-  for (int e = 0; e < 8; e++) red[rt][8 * ct + e] = sum[e];
+  for (int e = 0; e < 8; e++) red[rt * (8 * tpr) + 8 * ct + e] = sum[e];
   __syncthreads();
-  const int64_t col = (int64_t)blockIdx.y * kDzCols + threadIdx.x;
-  if (col >= a.n) return;
-  float s = red[0][threadIdx.x];
-#pragma unroll
-  for (int r = 1; r < 8; r++) s += red[r][threadIdx.x];
-  a.partial[(int64_t)blockIdx.x * a.n + col] = s;
+  for (int i = threadIdx.x; i < 8 * tpr && c0 + i < a.n; i += 256) {
+    float s = red[i];
+    for (int r = 1; r < rows; r++) s += red[r * (8 * tpr) + i];
+    a.partial[(int64_t)blockIdx.x * a.n + c0 + i] = s;
+  }
 }
 
 // dbias[g][j] = sum of the partial sums of group g's row tiles, in order within
@@ -229,11 +234,13 @@ __global__ __launch_bounds__(256) void dbias_kernel(DzArgs a, int64_t tiles, uin
 int64_t dz_tiles(int64_t m, int64_t groups) { return (m + kDzRows - 1) / kDzRows + groups; }
 
 template <int DT>
-hipError_t launch_dz(const DzArgs& a, int act, void* dbias, hipStream_t s) {
+hipError_t launch_dz(DzArgs a, int act, void* dbias, hipStream_t s) {
+  a.tpr = 8;
+  while (a.tpr < kDzThreads && 8 * a.tpr < a.n) a.tpr *= 2;
   const int64_t tiles = dz_tiles(a.m, a.groups);
   const bool vec = a.n % 8 == 0;
   if (a.m > 0 && (a.dz || dbias)) {
-    const dim3 grid((unsigned)tiles, (unsigned)((a.n + kDzCols - 1) / kDzCols));
+    const dim3 grid((unsigned)tiles, (unsigned)((a.n + 8 * a.tpr - 1) / (8 * a.tpr)));
     with_act(act, [&](auto ACT_) {
       constexpr int ACT = decltype(ACT_)::value;
       if (vec) dz_kernel<DT, ACT, true><<<grid, 256, 0, s>>>(a);
