@@ -9,24 +9,47 @@
 namespace mc2 {
 namespace lin {
 
+// A product runs in turns of one tile per CU; a turn takes a fixed time
+// (launch, first loads, epilogue) and a time per step of 64 of K, in us, as
+// fitted to 8192 x 4096 products of k = 1024 and 2048 (which take, us, with
+// the tiles in this order: 63 / 71 / 83 and 107 / 119 / 141; k = 256: 31 / 33 /
+// 43; 2048 x 2048 x 1024, which fills the CUs with small tiles only: 23 / 16 /
+// 14; 2048 x 4096 x 4096: 75 / 56 / 67).
+struct TurnTime { Tile tile; int bm, bn; double fixed, step; };
+constexpr TurnTime kTurns[] = {{TILE_256X256, 256, 256, 9.0, 1.39},
+                               {TILE_128X256, 128, 256, 5.5, 0.756},
+                               {TILE_128X128, 128, 128, 3.0, 0.456}};
+
 Plan plan_product(int64_t m, int64_t n, int64_t k, int gmode, int64_t groups) {
-  // turns of the 256 CUs times the time of one (linear_kernels.hpp), the
-  // groups' partial tiles taken as half of one each
-  auto tiles = [&](int64_t bm, int64_t bn) {
-    const double cols = (double)((n + bn - 1) / bn);
-    if (gmode == BY_ROWS) return ((double)m / (double)bm + 0.5 * (double)groups) * cols;
-    return (double)((m + bm - 1) / bm) * cols * (gmode == BY_K ? (double)groups : 1.0);
+  const double steps = std::ceil((double)k / (gmode == BY_K ? (double)groups : 1.0) / kStepK);
+  auto tiles = [&](const TurnTime& t) {
+    const double cols = (double)((n + t.bn - 1) / t.bn);
+    // groups of rows: each group's last tile taken as half a tile
+    if (gmode == BY_ROWS) return ((double)m / t.bm + 0.5 * (double)groups) * cols;
+    return (double)((m + t.bm - 1) / t.bm) * cols * (gmode == BY_K ? (double)groups : 1.0);
   };
-  auto cost = [&](int64_t bm, int64_t bn, double turn) { return std::ceil(tiles(bm, bn) / 256.0) * turn; };
-  const double c256 = cost(256, 256, 95.0), c128 = cost(128, 256, 56.0), small = cost(128, 128, 32.0);
   Plan p{TILE_128X128, 1, k, 0};
-  if (c256 <= c128 && c256 <= small) p.tile = TILE_256X256;
-  else if (c128 <= small) p.tile = TILE_128X256;
+  double best = -1.0;
+  for (const TurnTime& t : kTurns) {
+    const double cost = std::ceil(tiles(t) / 256.0) * (t.fixed + t.step * steps);
+    if (best < 0.0 || cost < best) {
+      best = cost;
+      p.tile = t.tile;
+    }
+  }
   if (p.tile != TILE_128X128 || gmode != DENSE) return p;
-  // split K where the tiles leave more than half of the CUs idle, in parts of
-  // 256 at least
-  const int64_t t = (int64_t)tiles(128, 128);
-  const int64_t s = std::min<int64_t>({256 / std::max<int64_t>(t, 1), k / 256, 32});
+  // Split K where that leaves CUs idle: fewer steps against a second launch
+  // (5 us) and the partial sums written and read (4 TB/s).
+  const int64_t t = (int64_t)tiles(kTurns[2]);
+  int64_t s = 1;
+  for (int64_t i = 2; i <= 32 && i * t <= 256; i++) {
+    const double cost = kTurns[2].fixed + kTurns[2].step * std::ceil(steps / (double)i) + 5.0 +
+                        (double)i * (double)m * (double)n * 8.0 / 4e6;
+    if (cost < best) {
+      best = cost;
+      s = i;
+    }
+  }
   if (s > 1) {
     p.k_part = ((k + s - 1) / s + kStepK - 1) / kStepK * kStepK;
     p.splits = (int)((k + p.k_part - 1) / p.k_part);

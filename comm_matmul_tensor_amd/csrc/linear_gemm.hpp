@@ -481,14 +481,16 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
   }
 
   if constexpr (GMODE == DENSE && BN < 256) {
-    if (p.splits > 1) {  // fp32 sums, tiles whole
+    if (p.splits > 1) {  // fp32 sums of the rows there are, whole tiles of columns
       const int64_t ld = (int64_t)tiles_n * BN;
       float* part = p.partial + ((int64_t)blockIdx.y * tiles_m * BM + m0 + wm * WM + lane % 16) * ld + n0 + wn * WN +
                     4 * (lane / 16);
 #pragma unroll
       for (int i = 0; i < FM; i++, part += 16 * ld)
+        if (m0 + wm * WM + 16 * i + lane % 16 < m_end) {
 #pragma unroll
-        for (int j = 0; j < FN; j++) *reinterpret_cast<f32x4*>(part + 16 * j) = acc[i][j];
+          for (int j = 0; j < FN; j++) *reinterpret_cast<f32x4*>(part + 16 * j) = acc[i][j];
+        }
       return;
     }
   }

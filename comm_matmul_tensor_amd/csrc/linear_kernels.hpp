@@ -6,10 +6,9 @@
 namespace mc2 {
 namespace lin {
 
-// The tiles, and how a product of k = 4096 runs with one of them on every CU:
-// 256 x 256 in two LDS stages 95 us, 128 x 256 in three 56 us, 128 x 128 in
-// four 32 us.  A larger tile reads less per product; a smaller one fills the
-// CUs better, and its deeper ring of stages covers more of the latency.
+// The tiles: 256 x 256 in two LDS stages, 128 x 256 in three, 128 x 128 in
+// four.  A larger tile reads less per product; a smaller one fills the CUs
+// better, and its deeper ring of stages covers more of the latency.
 enum Tile : int { TILE_256X256, TILE_128X256, TILE_128X128 };
 
 // Tile and split of a product, from its sizes alone (the workspace's size

@@ -7,7 +7,7 @@
 //            + the choices of e before i in i's own segment,
 // the last by a ballot per bit of the expert id (lanes with equal ids) and a
 // running count in LDS.  No step depends on the order of atomics (counts
-// only).  Up to kChunk choices take one workgroup and one launch (a decoding
+// only).  Up to kAlone choices take one workgroup and one launch (a decoding
 // batch is bound by launches); more take a count, a scan over the
 // workgroups' counts (one wavefront per expert) and a ranking launch.
 //
@@ -21,7 +21,11 @@
 namespace mc2 {
 namespace {
 
-constexpr int kChunk = 8192;   // choices per workgroup of the sort
+// Choices that one workgroup sorts alone, and choices per workgroup where there
+// are more.  32768 choices with their rows (h = 4096): chunks of 8192 / 4096 /
+// 2048 / 1024 take 68 / 64 / 62 / 61 us; 524288 choices (h = 64) 46 / 43 / 46 /
+// 56.  2048 or 8192 choices alone: 13 us a call, 20 in three launches.
+constexpr int kAlone = 8192, kChunk = 2048;
 // Workgroups that walk the tokens of the gradient: enough to fill the CUs
 // once.  More in flight only scatter the rows read and written at a time:
 // 8192 tokens, 4 choices, h = 4096: 1024 workgroups 125 us, 2048 130, 4096
@@ -362,7 +366,7 @@ __global__ __launch_bounds__(256) void unpermute_grad(UnpermuteArgs a, int64_t t
   }
 }
 
-int64_t sort_blocks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t sort_blocks(int64_t n) { return n <= kAlone ? 1 : (n + kChunk - 1) / kChunk; }
 
 template <int DT, bool VEC>
 hipError_t unpermute_launch(const UnpermuteArgs& a, hipStream_t s) {

@@ -24,9 +24,10 @@ namespace {
 
 enum : int { OUT_16 = 0, OUT_I8 = 1, OUT_F8 = 2 };
 
-// Codes of eight values with the scale of absmax bits `top_bits` (|y| as an
-// integer, so that NaN and infinity come out as the maximum); 8 bytes.
-// The division is the IEEE one: the codes are those of the formula.
+// Codes of eight values; 8 bytes.  `usable`: the scale is positive and finite.
+// The division is the IEEE one, so that the codes are those of the formula;
+// products with the inverse, divided again only near a rounding boundary, took
+// 15.5 us against 16.0 for 1023 x 7168: the kernel waits for memory.
 template <int OUT>
 __device__ __forceinline__ u32x2 codes8(const float (&y)[8], float scale, bool usable) {
   constexpr float kTop = OUT == OUT_I8 ? 127.0f : 448.0f;
@@ -47,6 +48,8 @@ __device__ __forceinline__ u32x2 codes8(const float (&y)[8], float scale, bool u
   }
   return r;
 }
+// Scale of a group from its largest |y|, compared as an integer, so that a NaN
+// or an infinity comes out as the maximum.
 template <int OUT>
 __device__ __forceinline__ float scale_of(uint32_t top_bits) {
   return __uint_as_float(top_bits) / (OUT == OUT_I8 ? 127.0f : 448.0f);
