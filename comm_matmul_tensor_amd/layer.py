@@ -19,10 +19,10 @@ from . import (_I64, _INT, _P, _TORCH_DT, _check, _lib, _stream_obj)
 
 MC2_ACT_NONE, MC2_ACT_RELU, MC2_ACT_GELU, MC2_ACT_GELU_TANH, MC2_ACT_SILU = range(5)
 
-_SZ, _F32 = ctypes.c_size_t, ctypes.c_float
+_SZ, _FLT = ctypes.c_size_t, ctypes.c_float
 _SZP = ctypes.POINTER(ctypes.c_size_t)
 _SIGS = {
-    "mc2_add_rms_norm": [_P, _P, _P, _I64, _I64, _INT, _F32, _P, _INT, _P, _I64, _P, _P, _P],
+    "mc2_add_rms_norm": [_P, _P, _P, _I64, _I64, _INT, _FLT, _P, _INT, _P, _I64, _P, _P, _P],
     "mc2_add_rms_norm_grad_workspace_size": [_I64, _I64, _SZP],
     "mc2_add_rms_norm_grad": [_P, _P, _P, _P, _P, _I64, _I64, _INT, _P, _P, _P, _SZ, _P],
     "mc2_linear_act_workspace_size": [_I64, _I64, _I64, _I64, _SZP],
@@ -40,6 +40,8 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 
 _HALF = (torch.float16, torch.bfloat16)
+_EIGHT = (torch.int8, torch.float8_e4m3fn)
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _tensor(t, name: str, dim: Optional[int] = None):
@@ -56,9 +58,7 @@ def _half(t, name: str):
 
 
 def _like(t, name: str, shape, dtype):
-    """An optional argument's shape and dtype (the C ABI sees only pointers and sizes)."""
-    if t is None:
-        return
+    """An argument's shape and dtype (the C ABI sees only pointers and sizes)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
@@ -70,36 +70,41 @@ def _like(t, name: str, shape, dtype):
 def _needed(t, name: str, shape, dtype):
     if t is None:
         raise ValueError(f"{name} is required")
-    _like(t, name, shape, dtype)
+    if t is not None:
+        _like(t, name, shape, dtype)
 
 
 def _place(names: str, *tensors) -> int:
     """The current stream's handle, after checking that every tensor is contiguous and on the
-    current device (a decoding step's calls are short, so the checks are kept few and cheap)."""
-    given = [t for t in tensors if t is not None]
-    for t in given:
-        if not t.is_contiguous():
-            raise ValueError(f"{_name(names, t, tensors)} must be contiguous")
-    dev = None
-    for t in given:
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError(f"{_name(names, t, tensors)} must be a device tensor")
-            if dev is not None:
-                raise ValueError(f"{_name(names, t, tensors)} is on {t.device}, the other tensors on cuda:{dev}")
-            dev = d
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev} but the current device is cuda:{torch.cuda.current_device()}")
+    current device (a decoding step's calls take a few microseconds: the checks are one pass)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            _refuse(names, tensors)
+    if dev < 0 or dev != _current_device():
+        _refuse(names, tensors)
     return torch.cuda.current_stream(dev).cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
-# the handle alone, without the Stream object around it
+def _refuse(names: str, tensors):
+    named = [(name, t) for name, t in zip(names.split(), tensors) if t is not None]
+    for name, t in named:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    dev = None
+    for name, t in named:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        dev = t.device
+    raise ValueError(f"tensors are on {dev} but the current device is cuda:{torch.cuda.current_device()}")
+
+
+# the handle alone, without the Stream object around it, and the device without the check for a
+# first use (a tensor on it is at hand)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _name(names: str, t, tensors) -> str:
-    return names.split()[next(i for i, u in enumerate(tensors) if u is t)]
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(stream, fn, *args, **kwargs):
@@ -163,30 +168,35 @@ def mc2_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[t
         out_dtype = out.dtype
     elif out_dtype is None:
         out_dtype = dt
-    eight = out_dtype in (torch.int8, torch.float8_e4m3fn)
+    eight = out_dtype in _EIGHT
     if not eight and out_dtype != dt:
         raise TypeError(f"out_dtype must be {dt}, int8 or float8_e4m3fn, got {out_dtype}")
     if group not in (0, 128) or (group and (not eight or h % 128)):
         raise ValueError("group must be 0, or 128 with an 8-bit output and a multiple of 128 columns")
     scales = (rows, h // group if group else 1)
     _needed(weight, "weight", (h,), dt)
-    _like(residual, "residual", shape, dt)
-    _like(out, "out", shape, out_dtype)
-    _like(sum_out, "sum_out", shape, dt)
-    _like(rstd_out, "rstd_out", (rows,), torch.float32)
-    if scale_out is not None and not eight:
-        raise ValueError("scale_out goes with an 8-bit output")
-    _like(scale_out, "scale_out", scales, torch.float32)
+    if residual is not None:
+        _like(residual, "residual", shape, dt)
+    if out is not None:
+        _like(out, "out", shape, out_dtype)
+    if sum_out is not None:
+        _like(sum_out, "sum_out", shape, dt)
+    if rstd_out is not None:
+        _like(rstd_out, "rstd_out", (rows,), _F32)
+    if scale_out is not None:
+        if not eight:
+            raise ValueError("scale_out goes with an 8-bit output")
+        _like(scale_out, "scale_out", scales, _F32)
     handle = _place("x weight residual out scale_out sum_out rstd_out", x, weight, residual, out, scale_out, sum_out,
                     rstd_out)
     if out is None:
         out = torch.empty_like(x) if not eight else x.new_empty(shape, dtype=out_dtype)
     if eight and scale_out is None:
-        scale_out = x.new_empty(scales, dtype=torch.float32)
+        scale_out = x.new_empty(scales, dtype=_F32)
     if residual is not None and sum_out is None:
         sum_out = torch.empty_like(x)
     if need_rstd and rstd_out is None:
-        rstd_out = x.new_empty((rows,), dtype=torch.float32)
+        rstd_out = x.new_empty((rows,), dtype=_F32)
     _check(_lib.mc2_add_rms_norm(x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, h, _TORCH_DT[dt], eps,
                                  out.data_ptr(), _TORCH_DT[out_dtype], _ptr(scale_out), group, _ptr(sum_out),
                                  _ptr(rstd_out), handle))
@@ -211,10 +221,13 @@ def mc2_add_rms_norm_grad(dout: torch.Tensor, s: torch.Tensor, weight: torch.Ten
     dt = s.dtype
     _needed(dout, "dout", shape, dt)
     _needed(weight, "weight", (h,), dt)
-    _needed(rstd, "rstd", (rows,), torch.float32)
-    _like(dsum, "dsum", shape, dt)
-    _like(dx, "dx", shape, dt)
-    _like(dweight, "dweight", (h,), dt)
+    _needed(rstd, "rstd", (rows,), _F32)
+    if dsum is not None:
+        _like(dsum, "dsum", shape, dt)
+    if dx is not None:
+        _like(dx, "dx", shape, dt)
+    if dweight is not None:
+        _like(dweight, "dweight", (h,), dt)
     _workspace_ok(workspace)
     handle = _place("dout s weight rstd dsum dx dweight workspace", dout, s, weight, rstd, dsum, dx, dweight, workspace)
     _ws, ws, ws_bytes = _workspace(workspace, s, _lib.mc2_add_rms_norm_grad_workspace_size, rows, h)
@@ -237,7 +250,7 @@ def _linear_sizes(x, w, group_offsets):
         groups = size - 1
         if groups < 1:
             raise ValueError("group_offsets must hold at least 2 values")
-        if group_offsets.dtype != torch.int32:
+        if group_offsets.dtype != _I32:
             raise TypeError(f"group_offsets has dtype {group_offsets.dtype}, expected torch.int32")
     n = _tensor(w, "w", 3 if groups else 2)[-2]
     _needed(w, "w", (groups, n, k) if groups else (n, k), x.dtype)
@@ -261,10 +274,14 @@ def mc2_linear_act(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
                    out=out, z_out=z_out, workspace=workspace)
     m, k, n, groups = _linear_sizes(x, w, group_offsets)
     dt = x.dtype
-    _like(bias, "bias", (groups, n) if groups else (n,), dt)
-    _like(residual, "residual", (m, n), dt)
-    _like(out, "out", (m, n), dt)
-    _like(z_out, "z_out", (m, n), dt)
+    if bias is not None:
+        _like(bias, "bias", (groups, n) if groups else (n,), dt)
+    if residual is not None:
+        _like(residual, "residual", (m, n), dt)
+    if out is not None:
+        _like(out, "out", (m, n), dt)
+    if z_out is not None:
+        _like(z_out, "z_out", (m, n), dt)
     _workspace_ok(workspace)
     handle = _place("x w bias residual group_offsets out z_out workspace", x, w, bias, residual, group_offsets, out,
                     z_out, workspace)
@@ -295,11 +312,14 @@ def mc2_linear_act_grad(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, z:
     _needed(dout, "dout", (m, n), dt)
     if act != MC2_ACT_NONE:
         _needed(z, "z", (m, n), dt)
-    else:
+    elif z is not None:
         _like(z, "z", (m, n), dt)
-    _like(dx, "dx", (m, k), dt)
-    _like(dw, "dw", w.shape, dt)
-    _like(dbias, "dbias", bias_shape, dt)
+    if dx is not None:
+        _like(dx, "dx", (m, k), dt)
+    if dw is not None:
+        _like(dw, "dw", w.shape, dt)
+    if dbias is not None:
+        _like(dbias, "dbias", bias_shape, dt)
     _workspace_ok(workspace)
     handle = _place("dout x w z group_offsets dx dw dbias workspace", dout, x, w, z, group_offsets, dx, dw, dbias,
                     workspace)
@@ -329,10 +349,13 @@ def mc2_moe_permute(x: torch.Tensor, expert_ids: torch.Tensor, experts: int, *, 
     tokens, h = _tensor(x, "x", 2)
     _half(x, "x")
     top = _tensor(expert_ids, "expert_ids", 2)[1]
-    _needed(expert_ids, "expert_ids", (tokens, top), torch.int32)
-    _like(out, "out", (tokens * top, h), x.dtype)
-    _like(row_map, "row_map", (tokens, top), torch.int32)
-    _like(offsets, "offsets", (experts + 1,), torch.int32)
+    _needed(expert_ids, "expert_ids", (tokens, top), _I32)
+    if out is not None:
+        _like(out, "out", (tokens * top, h), x.dtype)
+    if row_map is not None:
+        _like(row_map, "row_map", (tokens, top), _I32)
+    if offsets is not None:
+        _like(offsets, "offsets", (experts + 1,), _I32)
     _workspace_ok(workspace)
     handle = _place("x expert_ids out row_map offsets workspace", x, expert_ids, out, row_map, offsets, workspace)
     _ws, ws, ws_bytes = _workspace(workspace, x, _lib.mc2_moe_permute_workspace_size, tokens, top, experts)
@@ -356,9 +379,11 @@ def mc2_moe_unpermute(y: torch.Tensor, row_map: torch.Tensor, weights: Optional[
     rows, h = _tensor(y, "y", 2)
     _half(y, "y")
     tokens, top = _tensor(row_map, "row_map", 2)
-    _needed(row_map, "row_map", (tokens, top), torch.int32)
-    _like(weights, "weights", (tokens, top), torch.float32)
-    _like(out, "out", (tokens, h), y.dtype)
+    _needed(row_map, "row_map", (tokens, top), _I32)
+    if weights is not None:
+        _like(weights, "weights", (tokens, top), _F32)
+    if out is not None:
+        _like(out, "out", (tokens, h), y.dtype)
     handle = _place("y row_map weights out", y, row_map, weights, out)
     if out is None:
         out = y.new_empty((tokens, h))
@@ -378,16 +403,19 @@ def mc2_moe_unpermute_grad(dout: torch.Tensor, y: torch.Tensor, row_map: torch.T
     rows, h = _tensor(y, "y", 2)
     _half(y, "y")
     tokens, top = _tensor(row_map, "row_map", 2)
-    _needed(row_map, "row_map", (tokens, top), torch.int32)
+    _needed(row_map, "row_map", (tokens, top), _I32)
     _needed(dout, "dout", (tokens, h), y.dtype)
-    _like(weights, "weights", (tokens, top), torch.float32)
-    _like(dy, "dy", (rows, h), y.dtype)
-    _like(dweights, "dweights", (tokens, top), torch.float32)
+    if weights is not None:
+        _like(weights, "weights", (tokens, top), _F32)
+    if dy is not None:
+        _like(dy, "dy", (rows, h), y.dtype)
+    if dweights is not None:
+        _like(dweights, "dweights", (tokens, top), _F32)
     handle = _place("dout y row_map weights dy dweights", dout, y, row_map, weights, dy, dweights)
     if dy is None:
         dy = torch.empty_like(y)
     if need_dweights and dweights is None:
-        dweights = y.new_empty((tokens, top), dtype=torch.float32)
+        dweights = y.new_empty((tokens, top), dtype=_F32)
     _check(_lib.mc2_moe_unpermute_grad(dout.data_ptr(), y.data_ptr(), row_map.data_ptr(), _ptr(weights), tokens, top,
                                        h, rows, _TORCH_DT[y.dtype], dy.data_ptr(), _ptr(dweights), handle))
     return dy, dweights
