@@ -12,7 +12,7 @@ namespace {
 using std::string;
 
 constexpr int64_t kRows = (int64_t)1 << 24, kWidth = (int64_t)1 << 24, kDim = (int64_t)1 << 21,
-                  kTokens = (int64_t)1 << 23, kGroups = 4096;
+                  kTokens = (int64_t)1 << 23, kGroups = 4096, kGroupWidth = (int64_t)1 << 29;
 
 bool is_half(mc2_dtype d) { return d == MC2_F16 || d == MC2_BF16; }
 string str(int64_t v) { return std::to_string(static_cast<long long>(v)); }
@@ -89,6 +89,9 @@ mc2_status check_linear_sizes(const char* who, int64_t m, int64_t k, int64_t n, 
   if (k < 1 || k > kDim) return shape(who, "k must lie in [1, 2^21], got " + str(k));
   if (n < 1 || n > kDim) return shape(who, "n must lie in [1, 2^21], got " + str(n));
   if (groups < 0 || groups > kGroups) return shape(who, "groups must lie in [0, 4096], got " + str(groups));
+  // (every group may have a partial tile of rows: bounds the tiles of a launch)
+  if (groups * n > kGroupWidth || groups * k > kGroupWidth)
+    return shape(who, "groups * n and groups * k must be at most 2^29");
   return MC2_OK;
 }
 

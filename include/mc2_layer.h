@@ -91,7 +91,7 @@ typedef enum {
  * z_out     (m, n) of dtype or NULL: z rounded, which the gradient needs
  * workspace 16-byte aligned, at least mc2_linear_act_workspace_size bytes
  *           (NULL when that is 0)
- * m < 2^24, 1 <= k, n <= 2^21, G <= 4096.
+ * m < 2^24, 1 <= k, n <= 2^21, G <= 4096, G n and G k <= 2^29.
  */
 mc2_status mc2_linear_act_workspace_size(int64_t m, int64_t k, int64_t n, int64_t groups, size_t* bytes);
 mc2_status mc2_linear_act(const void* x, const void* w, const void* bias, const void* residual, int64_t m,

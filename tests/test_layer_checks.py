@@ -203,6 +203,7 @@ def test_linear_abi():
     assert fwd(k=0) == ERR_SHAPE and fwd(k=(1 << 21) + 1) == ERR_SHAPE
     assert fwd(n=0) == ERR_SHAPE and fwd(n=(1 << 21) + 1) == ERR_SHAPE
     assert fwd(g=-1) == ERR_SHAPE and fwd(g=4097, off=A) == ERR_SHAPE
+    assert fwd(g=4096, off=A, n=1 << 18) == ERR_SHAPE and fwd(g=4096, off=A, k=1 << 18) == ERR_SHAPE
     assert fwd(g=3) == ERR_NULL and fwd(off=A) == ERR_SHAPE
     assert fwd(dt=0) == ERR_DTYPE and fwd(act=5) == ERR_UNSUPPORTED and fwd(act=-1) == ERR_UNSUPPORTED
     for k in ("x", "w", "out"):
