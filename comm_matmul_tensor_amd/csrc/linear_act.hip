@@ -65,20 +65,32 @@ int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------- ragged rows
-// dst (rows, ld) = src (rows, k) with zeros in columns k .. ld - 1.
-__global__ __launch_bounds__(256) void pad_rows(const uint16_t* src, int64_t rows, int64_t k, int64_t ld,
-                                                uint16_t* dst) {
-  const int64_t chunks = ld / 8;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * chunks; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / chunks, c = i % chunks * 8;
-    *reinterpret_cast<u32x4*>(dst + row * ld + c) = load_chunk<false>(src + row * k, c, k);
+// dst (rows, ld) = src (rows, k) with zeros in columns k .. ld - 1, for up to
+// two matrices in one launch.
+struct PadArgs {
+  const uint16_t* src[2];
+  uint16_t* dst[2];
+  int64_t rows[2];
+  int64_t k, ld;
+};
+__global__ __launch_bounds__(256) void pad_rows(PadArgs a) {
+  const int64_t chunks = a.ld / 8, first = a.rows[0] * chunks, all = first + a.rows[1] * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int which = i >= first;
+    const int64_t j = which ? i - first : i, row = j / chunks, c = j % chunks * 8;
+    *reinterpret_cast<u32x4*>(a.dst[which] + row * a.ld + c) = load_chunk<false>(a.src[which] + row * a.k, c, a.k);
   }
 }
-hipError_t launch_pad_rows(const void* src, int64_t rows, int64_t k, void* dst, hipStream_t s) {
-  const int64_t chunks = rows * (pad8(k) / 8);
+hipError_t launch_pad_rows(const void* s0, int64_t rows0, void* d0, const void* s1, int64_t rows1, void* d1, int64_t k,
+                           hipStream_t s) {
+  const PadArgs a{{static_cast<const uint16_t*>(s0), static_cast<const uint16_t*>(s1)},
+                  {static_cast<uint16_t*>(d0), static_cast<uint16_t*>(d1)},
+                  {rows0, rows1},
+                  k,
+                  pad8(k)};
+  const int64_t chunks = (rows0 + rows1) * (pad8(k) / 8);
   if (chunks == 0) return hipSuccess;
-  pad_rows<<<(unsigned)std::min<int64_t>((chunks + 255) / 256, 256 * 16), 256, 0, s>>>(
-      static_cast<const uint16_t*>(src), rows, k, pad8(k), static_cast<uint16_t*>(dst));
+  pad_rows<<<(unsigned)std::min<int64_t>((chunks + 255) / 256, 256 * 16), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -343,8 +355,8 @@ hipError_t forward_dt(const LinearArgs& a, hipStream_t s) {
   p.lda = p.ldb = pad8(a.k);
   p.b_group = a.n * p.ldb;
   if (a.k % 8) {
-    hipError_t e = launch_pad_rows(a.x, a.m, a.k, ws + at.x8, s);
-    if (e == hipSuccess) e = launch_pad_rows(a.w, std::max<int64_t>(a.groups, 1) * a.n, a.k, ws + at.w8, s);
+    const hipError_t e = launch_pad_rows(a.x, a.m, ws + at.x8, a.w, std::max<int64_t>(a.groups, 1) * a.n, ws + at.w8,
+                                         a.k, s);
     if (e != hipSuccess) return e;
     p.a = ws + at.x8;
     p.b = ws + at.w8;
@@ -374,15 +386,11 @@ hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
   if (e != hipSuccess || !products) return e;
   const void *x = a.x, *w = a.w, *dz = copy ? d.dz : a.dout;
   if (a.k % 8) {
-    if (a.dw) {
-      e = launch_pad_rows(a.x, a.m, a.k, ws + at.x8, s);
-      x = ws + at.x8;
-    }
-    if (e == hipSuccess && a.dx) {
-      e = launch_pad_rows(a.w, matrices * a.n, a.k, ws + at.w8, s);
-      w = ws + at.w8;
-    }
+    // x for dw, w for dx
+    e = launch_pad_rows(a.x, a.dw ? a.m : 0, ws + at.x8, a.w, a.dx ? matrices * a.n : 0, ws + at.w8, a.k, s);
     if (e != hipSuccess) return e;
+    x = ws + at.x8;
+    w = ws + at.w8;
   }
   Product p{};
   p.offsets = a.offsets;

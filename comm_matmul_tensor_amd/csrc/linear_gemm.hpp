@@ -441,6 +441,24 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     __builtin_amdgcn_sched_barrier(0);
     half(la1, la0, fb1, fb0, std::integral_constant<bool, true>(), cur, kt + NS, nxt, 0);
   };
+  // The residual's values of this lane.  Where a wavefront has registers for
+  // them they are loaded before the main loop, which hides their latency
+  // (517 x 1792 x 4096 in fp16: 17.9 -> 17.4 us; 15.8 without a residual).
+  const uint16_t* residual = static_cast<const uint16_t*>(p.residual);
+  const bool quads = p.n % 4 == 0;
+  const int64_t col0 = n0 + wn * WN + 4 * (lane / 16);  // this lane's first column
+  auto load_residual = [&](int i, u32x2(&rv)[FN]) {
+    const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
+#pragma unroll
+    for (int j = 0; j < FN; j++)
+      rv[j] = load4(residual + row * p.n + col0 + 16 * j, row < m_end ? p.n - col0 - 16 * j : 0, quads);
+  };
+  constexpr bool kEarly = FM * FN <= 16;
+  u32x2 early[kEarly ? FM : 1][FN];
+  if (kEarly && residual && (GMODE != DENSE || p.splits < 2)) {
+#pragma unroll
+    for (int i = 0; i < (kEarly ? FM : 1); i++) load_residual(i, early[i]);
+  }
   if (nk > 0) {
     uint8_t* const st[4] = {s0, s1, s2, s3};
 #pragma unroll
@@ -503,8 +521,6 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     const int row = wm * WM + 16 * i + lane % 16, col = wn * WN + 16 * j + 4 * (lane / 16);
     return reinterpret_cast<u32x2*>((row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col);
   };
-  const bool quads = p.n % 4 == 0;
-  const int64_t col0 = n0 + wn * WN + 4 * (lane / 16);  // this lane's first column
   if (bias) {
 #pragma unroll
     for (int j = 0; j < FN; j++) {
@@ -526,25 +542,19 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     store_tile<BM, BN, NT>(h0, h1, static_cast<uint16_t*>(p.z) + c_shift, m0, m_end, n0, p.n);
     __syncthreads();
   }
-  const uint16_t* residual = static_cast<const uint16_t*>(p.residual);
   with_act(p.act, [&](auto ACT_) {
     constexpr int ACT = decltype(ACT_)::value;
 #pragma unroll
     for (int i = 0; i < FM; i++) {
-      const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
-      u32x2 rv[FN];
-      if (residual) {
-#pragma unroll
-        for (int j = 0; j < FN; j++)
-          rv[j] = load4(residual + row * p.n + col0 + 16 * j, row < m_end ? p.n - col0 - 16 * j : 0, quads);
-      }
+      u32x2 late[FN];
+      if (!kEarly && residual) load_residual(i, late);
 #pragma unroll
       for (int j = 0; j < FN; j++) {
         f32x4 v = acc[i][j];
 #pragma unroll
         for (int r = 0; r < 4; r++) v[r] = act_of<ACT>(v[r]);
         if (residual) {
-          const f32x4 f = widen4<DT>(rv[j]);
+          const f32x4 f = widen4<DT>(kEarly ? early[kEarly ? i : 0][j] : late[j]);
 #pragma unroll
           for (int r = 0; r < 4; r++) v[r] += f[r];
         }
