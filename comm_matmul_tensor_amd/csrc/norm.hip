@@ -10,10 +10,11 @@
 //
 // Forward: a row is held by TPR threads with NCH chunks each, one row per
 // team, as many teams as rows.  Rows of up to 1024 columns take one wavefront
-// (no barrier, four rows per workgroup), wider ones a workgroup of 256 or 1024
+// (no barrier, four rows per workgroup), wider ones a workgroup of 256 to 1024
 // threads; rows of more than 32768 columns, which do not fit, are read again
-// for every pass (norm_wide).  8192 x 7168 with residual: 80 us, 5.9 TB/s (a
-// large copy reaches 5.2); 512 to 2048 workgroups that walk the rows: 85 to 87.
+// for every pass (norm_wide).  8192 x 7168 with residual: 79.5 us, 5.9 TB/s (a
+// large copy reaches 5.2) with 512 threads per row, 80.4 with 256, 81 with
+// 1024; 512 to 2048 workgroups that walk the rows: 85 to 87.
 #include <algorithm>
 
 #include "layer_device.hpp"
@@ -27,7 +28,7 @@ enum : int { OUT_16 = 0, OUT_I8 = 1, OUT_F8 = 2 };
 // Codes of eight values; 8 bytes.  `usable`: the scale is positive and finite.
 // The division is the IEEE one, so that the codes are those of the formula;
 // products with the inverse, divided again only near a rounding boundary, took
-// 15.5 us against 16.0 for 1023 x 7168: the kernel waits for memory.
+// 0.5 us of 16 off 1023 x 7168: the kernel waits for memory.
 template <int OUT>
 __device__ __forceinline__ u32x2 codes8(const float (&y)[8], float scale, bool usable) {
   constexpr float kTop = OUT == OUT_I8 ? 127.0f : 448.0f;
@@ -251,8 +252,8 @@ hipError_t norm_launch(const NormArgs& a, hipStream_t st) {
   if (h <= 512) wave(integral_constant<int, 1>());
   else if (h <= 1024) wave(integral_constant<int, 2>());
   else if (h <= 2048) norm_kernel<DT, 256, 1, OUT, VEC><<<(unsigned)a.rows, 256, 0, st>>>(a);
-  else if (h <= 4096) norm_kernel<DT, 256, 2, OUT, VEC><<<(unsigned)a.rows, 256, 0, st>>>(a);
-  else if (h <= 8192) norm_kernel<DT, 256, 4, OUT, VEC><<<(unsigned)a.rows, 256, 0, st>>>(a);
+  else if (h <= 4096) norm_kernel<DT, 512, 1, OUT, VEC><<<(unsigned)a.rows, 512, 0, st>>>(a);
+  else if (h <= 8192) norm_kernel<DT, 512, 2, OUT, VEC><<<(unsigned)a.rows, 512, 0, st>>>(a);
   else if (h <= 16384) norm_kernel<DT, 1024, 2, OUT, VEC><<<(unsigned)a.rows, 1024, 0, st>>>(a);
   else if (h <= 32768) norm_kernel<DT, 1024, 4, OUT, VEC><<<(unsigned)a.rows, 1024, 0, st>>>(a);
   else norm_wide<DT, OUT, VEC><<<(unsigned)a.rows, kWide, 0, st>>>(a);
