@@ -50,7 +50,7 @@ hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
   const int64_t tiles_m = (p.m + BM - 1) / BM + (GMODE == BY_ROWS ? p.groups : 0), tiles_n = (p.n + BN - 1) / BN;
   p.splits = plan.splits;
   p.k_part = plan.k_part;
-  p.order_cols = gemm::prefer_column_order(p.m, p.n, p.k, 2) ? 1 : 0;
+  p.order_cols = GMODE != BY_ROWS && gemm::prefer_column_order(p.m, p.n, p.k, 2) ? 1 : 0;
   p.tile_group = gemm::choose_tile_group(tiles_m * BM, p.n, BM, BN, p.order_cols);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)(GMODE == BY_K ? p.groups : plan.splits));
   product_kernel<DT, BM, BN, WGM, WGN, NS, AK, BK, GMODE><<<grid, 64 * WGM * WGN, 0, s>>>(p);

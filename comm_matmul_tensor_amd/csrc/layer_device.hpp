@@ -95,6 +95,30 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return max(v, (uint32_t)__shfl_xor((int)v, 32));
 }
 
+// Inclusive scans over the wavefront's lanes (sums; maxima of values >= 0):
+// within rows of 16 lanes, then from each row into the next, then from the
+// lower 32 lanes into the upper.  Lanes a step does not reach combine with 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_0(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan_add(int v) {
+  v += dpp_or_0<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v += dpp_or_0<0x112, 0xF>(v);
+  v += dpp_or_0<0x114, 0xF>(v);
+  v += dpp_or_0<0x118, 0xF>(v);
+  v += dpp_or_0<0x142, 0xA>(v);  // row_bcast 15
+  return v + dpp_or_0<0x143, 0xC>(v);  // row_bcast 31
+}
+__device__ __forceinline__ int wave_scan_max(int v) {
+  v = max(v, dpp_or_0<0x111, 0xF>(v));
+  v = max(v, dpp_or_0<0x112, 0xF>(v));
+  v = max(v, dpp_or_0<0x114, 0xF>(v));
+  v = max(v, dpp_or_0<0x118, 0xF>(v));
+  v = max(v, dpp_or_0<0x142, 0xA>(v));
+  return max(v, dpp_or_0<0x143, 0xC>(v));
+}
+
 // Sum / maximum over the WAVES wavefronts of a workgroup in wavefront order.
 // `red` (WAVES slots) must not be in use by an earlier call: callers that
 // reduce repeatedly alternate between arrays, so that one barrier between

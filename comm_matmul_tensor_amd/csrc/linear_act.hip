@@ -243,18 +243,11 @@ __global__ __launch_bounds__(256) void dbias_kernel(DzArgs a, int64_t tiles, uin
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int64_t j = (int64_t)blockIdx.x * 64 + lane;
   int64_t first = 0, count = tiles;
-  if (a.groups > 0) {  // tiles of the groups before this one, and its own
-    const int64_t g = blockIdx.y;
-    int64_t begin = 0;
-    count = 0;
-    for (int64_t i = 0; i <= g; i++) {
-      int64_t end = a.offsets[i + 1];
-      end = end < begin ? begin : end > a.m ? a.m : end;
-      first += count;
-      count = (end - begin + kDzRows - 1) / kDzRows;
-      begin = end;
-    }
-    dbias += g * a.n;
+  if (a.groups > 0) {
+    const GroupAt g = group_at(a.offsets, a.groups, a.m, kDzRows, blockIdx.y);
+    first = g.first;
+    count = g.count;
+    dbias += blockIdx.y * a.n;
   }
   float s = 0.0f;
   if (j < a.n) {

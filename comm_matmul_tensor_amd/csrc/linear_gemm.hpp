@@ -28,8 +28,8 @@
 // B and bias; for the weight's gradient the groups are ranges of K.  A tile
 // that crosses the end of its rows, columns or K reads zeros or repeats its
 // last column, and stores nothing outside.  32 experts of 4096 x 1792 over
-// 16384 rows: 290 us; 231 if all had one matrix, so a fifth of the time is
-// their 470 MB coming from HBM while the product waits.
+// 16384 rows: 269 us; 231 if all had one matrix, the rest being their 470 MB
+// from HBM and the tiles that a group's rows do not fill.
 #pragma once
 #include <type_traits>
 
@@ -72,96 +72,78 @@ struct Product {
 
 enum : int { DENSE = 0, BY_ROWS = 1, BY_K = 2 };
 
-struct RowRange { int64_t group, begin, end, tile; };
+struct RowRange { int64_t group, begin, end, tile, tiles; };
 
 // A value below 2^31 that every lane holds, as a scalar (buffer resources and
 // loop bounds made from it need no loop over lanes).
 __device__ __forceinline__ int64_t uniform(int64_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
 
 // 64 groups from g0 on, one per lane: the rows [start, end) of the lane's
-// group and its tiles of bm rows.  Range ends are read as ascending and at
-// most m; `begin`, the end of the group before g0, becomes that of the last.
+// group, its tiles of bm rows, and the tiles of the 64 groups up to its own.
+// Range ends are read as ascending and at most m; `begin`, the end of the
+// group before g0, becomes that of the last.
 struct GroupTiles {
-  int64_t start, end;
-  int tiles;
+  int start, end, tiles, incl;
   __device__ __forceinline__ GroupTiles(const int32_t* offsets, int64_t groups, int64_t m, int bm, int64_t g0,
-                                        int64_t& begin) {
+                                        int& begin) {
     const int lane = threadIdx.x % 64;
-    int e = g0 + lane < groups ? offsets[g0 + lane + 1] : 0;
-    const int b = (int)begin;
-    e = e < b ? b : e > (int)m ? (int)m : e;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(e, d);
-      if (lane >= d && v > e) e = v;
-    }
-    int s = __shfl_up(e, 1);
-    if (lane == 0) s = b;
-    start = s;
-    end = e;
-    tiles = (e - s + bm - 1) / bm;
-    begin = uniform(__shfl(e, 63));
+    const int e = g0 + lane < groups ? offsets[g0 + lane + 1] : 0;
+    end = wave_scan_max(max(min(e, (int)m), begin));
+    start = __builtin_amdgcn_update_dpp(begin, end, 0x138, 0xF, 0xF, false);  // wave_shr 1; lane 0: begin
+    tiles = (end - start + bm - 1) / bm;
+    incl = wave_scan_add(tiles);
+    begin = __builtin_amdgcn_readlane(end, 63);
   }
+  __device__ __forceinline__ int total() const { return __builtin_amdgcn_readlane(incl, 63); }
 };
 
 // Tiles of bm rows over all groups (each counts its own) and over the rows
 // after the last group, which follow them.
-__device__ __forceinline__ int64_t count_tiles(const int32_t* offsets, int64_t groups, int64_t m, int bm) {
-  int64_t begin = 0;
-  int n = 0;
-  for (int64_t g0 = 0; g0 < groups; g0 += 64) n += GroupTiles(offsets, groups, m, bm, g0, begin).tiles;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-  return uniform(n + (m - begin + bm - 1) / bm);
+__device__ __forceinline__ int count_tiles(const int32_t* offsets, int64_t groups, int64_t m, int bm) {
+  int begin = 0, n = 0;
+  for (int64_t g0 = 0; g0 < groups; g0 += 64) n += GroupTiles(offsets, groups, m, bm, g0, begin).total();
+  return n + ((int)m - begin + bm - 1) / bm;
 }
 
-// Tile `tile` of them (group = groups: after the last group; a tile past them
-// all has begin + tile bm >= end).  Every wavefront finds it for itself.
-__device__ __forceinline__ RowRange find_tile(const int32_t* offsets, int64_t groups, int64_t m, int bm,
-                                              int64_t tile) {
-  const int lane = threadIdx.x % 64;
-  int64_t begin = 0;
-  int left = (int)tile;  // of the groups still to come
+// Tile `tile` of them, each counted `cols` times: the group (groups: the rows
+// after the last one), its rows, its tiles of bm rows, and the tile's place
+// among the group's tiles * cols (a place past them all: nothing there).
+// Every wavefront finds it for itself.
+__device__ __forceinline__ RowRange find_tile(const int32_t* offsets, int64_t groups, int64_t m, int bm, int tile,
+                                              int cols = 1) {
+  int begin = 0, left = tile;  // left: of the groups still to come
   for (int64_t g0 = 0; g0 < groups; g0 += 64) {
     const GroupTiles t(offsets, groups, m, bm, g0, begin);
-    int incl = t.tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
-    }
-    const unsigned long long hit = __ballot(left < incl);
+    const unsigned long long hit = __ballot(left < t.incl * cols);
     if (hit) {
       const int l = __ffsll((long long)hit) - 1;
       RowRange r;
       r.group = g0 + l;
-      r.begin = uniform(__shfl((int)t.start, l));
-      r.end = uniform(__shfl((int)t.end, l));
-      r.tile = uniform(left - __shfl(incl - t.tiles, l));
+      r.begin = __builtin_amdgcn_readlane(t.start, l);
+      r.end = __builtin_amdgcn_readlane(t.end, l);
+      r.tiles = __builtin_amdgcn_readlane(t.tiles, l);
+      r.tile = left - (__builtin_amdgcn_readlane(t.incl, l) - (int)r.tiles) * cols;
       return r;
     }
-    left -= __shfl(incl, 63);
+    left -= t.total() * cols;
   }
-  return RowRange{groups, begin, m, uniform(left)};
+  return RowRange{groups, begin, m, left, (m - begin + bm - 1) / bm};
 }
 
-// Range of group g: the ends as find_tile reads them.
-__device__ __forceinline__ void group_range(const int32_t* offsets, int64_t g, int64_t m, int64_t& begin,
-                                            int64_t& end) {
-  const int lane = threadIdx.x % 64;
-  int64_t top = 0;
-  for (int64_t i = lane; i < g; i += 64) {
-    const int64_t v = offsets[i + 1];
-    top = v > top ? v : top;
+// Rows [begin, end) of group g, as find_tile reads them, and its tiles of bm
+// rows: `count` from number `first` on.
+struct GroupAt { int64_t begin, end, first, count; };
+__device__ __forceinline__ GroupAt group_at(const int32_t* offsets, int64_t groups, int64_t m, int bm, int64_t g) {
+  int begin = 0, first = 0;
+  for (int64_t g0 = 0;; g0 += 64) {
+    const GroupTiles t(offsets, groups, m, bm, g0, begin);
+    if (g < g0 + 64) {
+      const int l = (int)(g - g0), count = __builtin_amdgcn_readlane(t.tiles, l);
+      return GroupAt{__builtin_amdgcn_readlane(t.start, l), __builtin_amdgcn_readlane(t.end, l),
+                     first + __builtin_amdgcn_readlane(t.incl, l) - count, count};
+    }
+    first += t.total();
   }
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int64_t v = __shfl_xor(top, d);
-    top = v > top ? v : top;
-  }
-  begin = uniform(top > m ? m : top);
-  const int64_t e = offsets[g + 1];
-  end = uniform(e < begin ? begin : e > m ? m : e);
 }
 
 // One operand's loads: R rows of MN and 64 of K per step by NT threads.
@@ -241,15 +223,17 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// Tile (tm, tn) of workgroup `block`: blocks are dealt to the 8 XCDs in turn,
-// so each XCD gets a contiguous eighth of the tiles, walked in bands of
-// `group` tile rows (columns with order_cols), across the band first: the
-// tiles an XCD runs at once share bands of A and of B in its L2.
-__device__ __forceinline__ void tile_at(int block, int tiles_m, int tiles_n, int order_cols, int group, int& tm,
+// Workgroup `block`'s place among the tiles: blocks are dealt to the 8 XCDs in
+// turn, so each XCD gets a contiguous eighth of them.
+__device__ __forceinline__ int tile_place(int block, int tiles) {
+  const int per = tiles / 8, extra = tiles % 8, xcd = block % 8;
+  return xcd * per + (xcd < extra ? xcd : extra) + block / 8;
+}
+// Tile (tm, tn) at that place: bands of `group` tile rows (columns with
+// order_cols) one after another, each walked across the band first, so that
+// the tiles an XCD runs at once share bands of A and of B in its L2.
+__device__ __forceinline__ void tile_at(int lin, int tiles_m, int tiles_n, int order_cols, int group, int& tm,
                                         int& tn) {
-  const int tiles = tiles_m * tiles_n;
-  const int per = tiles / 8, extra = tiles % 8, xcd = block % 8, at = block / 8;
-  const int lin = xcd * per + (xcd < extra ? xcd : extra) + at;
   const int n_major = order_cols ? tiles_n : tiles_m, n_minor = order_cols ? tiles_m : tiles_n;
   const int per_band = group * n_minor;
   const int first = (lin / per_band) * group;
@@ -338,26 +322,22 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
 
   // the tile, its rows of C, its matrices and its range of K
   const int tiles_n = (int)((p.n + BN - 1) / BN);
-  int tiles_m = (int)((p.m + BM - 1) / BM);
-  if constexpr (GMODE == BY_ROWS) {
-    // (the grid has room for a partial tile in every group; the tiles there
-    // are are spread over all XCDs)
-    tiles_m = (int)count_tiles(p.offsets, p.groups, p.m, BM);
-    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
-  }
-  int tm, tn;
-  tile_at((int)blockIdx.x, tiles_m, tiles_n, p.order_cols, p.tile_group, tm, tn);
-  const int64_t n0 = (int64_t)tn * BN;
-  int64_t m0 = (int64_t)tm * BM, m_end = p.m, k0 = 0, k_len = p.k;
+  int tiles_m = (int)((p.m + BM - 1) / BM), tm, tn;
+  int64_t m0, m_end = p.m, k0 = 0, k_len = p.k, c_shift = 0;
   const uint16_t* a = static_cast<const uint16_t*>(p.a);
   const uint16_t* b = static_cast<const uint16_t*>(p.b);
   const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
-  int64_t c_shift = 0;
   if constexpr (GMODE == BY_ROWS) {
-    const RowRange r = find_tile(p.offsets, p.groups, p.m, BM, tm);
-    m0 = r.begin + r.tile * BM;
+    // The grid has room for a partial tile in every group; the tiles there are
+    // go group by group, in bands of rows within each, spread over all XCDs.
+    // (Bands across groups had most groups' B read in two turns of the CUs: the
+    // 32 experts above took 290 us.)
+    tiles_m = count_tiles(p.offsets, p.groups, p.m, BM);
+    if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+    const RowRange r = find_tile(p.offsets, p.groups, p.m, BM, tile_place((int)blockIdx.x, tiles_m * tiles_n), tiles_n);
+    tile_at((int)r.tile, (int)r.tiles, tiles_n, 0, p.tile_group, tm, tn);
+    m0 = r.begin + (int64_t)tm * BM;
     m_end = r.end;
-    if (m0 >= m_end) return;
     if (r.group == p.groups) {  // rows of no group: z = 0
       k_len = 0;
       bias = nullptr;
@@ -365,16 +345,20 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
       b += r.group * p.b_group;
       if (bias) bias += r.group * p.n;
     }
-  } else if constexpr (GMODE == BY_K) {
-    const int64_t g = blockIdx.y;
-    int64_t end;
-    group_range(p.offsets, g, p.k, k0, end);
-    k_len = end - k0;
-    c_shift = g * p.m * p.n;
-  } else if (BN < 256 && p.splits > 1) {  // (the wider tiles are not split)
-    k0 = (int64_t)blockIdx.y * p.k_part;
-    k_len = p.k - k0 < p.k_part ? p.k - k0 : p.k_part;
+  } else {
+    tile_at(tile_place((int)blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, p.order_cols, p.tile_group, tm, tn);
+    m0 = (int64_t)tm * BM;
+    if constexpr (GMODE == BY_K) {
+      const GroupAt g = group_at(p.offsets, p.groups, p.k, 1, blockIdx.y);
+      k0 = g.begin;
+      k_len = g.end - g.begin;
+      c_shift = (int64_t)blockIdx.y * p.m * p.n;
+    } else if (BN < 256 && p.splits > 1) {  // (the wider tiles are not split)
+      k0 = (int64_t)blockIdx.y * p.k_part;
+      k_len = p.k - k0 < p.k_part ? p.k - k0 : p.k_part;
+    }
   }
+  const int64_t n0 = (int64_t)tn * BN;
 
   Loader<BM, AK, NT> da;
   Loader<BN, BK, NT> db;
