@@ -114,6 +114,21 @@ def test_forward_groups(mc2, m, offsets, k, n):
     run_forward(mc2, 22, m, k, n, "f16", "none", False, False, offsets, keep_z=False)
 
 
+def many_groups(m, groups):
+    """Ranges of 0 to 60 rows, every fifth one empty, one end out of order, rows left over."""
+    g = torch.Generator().manual_seed(groups)
+    sizes = torch.randint(0, 61, (groups,), generator=g)
+    sizes[::5] = 0
+    offsets = [0] + (sizes.cumsum(0) * (m - 9) // sizes.sum()).tolist()
+    offsets[groups // 2] = offsets[groups // 3]
+    return offsets
+
+
+def test_forward_many_groups(mc2):
+    run_forward(mc2, 24, 3000, 72, 136, "bf16", "silu", True, True, many_groups(3000, 700))
+    run_forward(mc2, 25, 9000, 64, 520, "f16", "none", True, False, many_groups(9000, 129))
+
+
 def test_forward_groups_large_tiles(mc2):
     run_forward(mc2, 23, 2500, 192, 2048, "bf16", "gelu", True, False, [0, 700, 1500, 1501, 2470])
 
@@ -190,6 +205,11 @@ def test_grad_groups(mc2, m, offsets, k, n):
     print(f"grad groups m={m} k={k} n={n} offsets={offsets[:8]}", flush=True)
     run_grad(mc2, 33, m, k, n, "bf16", "silu", offsets)
     run_grad(mc2, 34, m, k, n, "f16", "none", offsets)
+
+
+def test_grad_many_groups(mc2):
+    run_grad(mc2, 36, 3000, 72, 136, "bf16", "silu", many_groups(3000, 700))
+    run_grad(mc2, 37, 9000, 64, 520, "f16", "gelu", many_groups(9000, 129))
 
 
 def test_grad_groups_large_tiles(mc2):
