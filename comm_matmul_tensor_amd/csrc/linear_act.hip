@@ -9,18 +9,22 @@
 namespace mc2 {
 namespace lin {
 
-// A product runs in turns of one tile per CU; a turn takes a fixed time
-// (launch, first loads, epilogue) and a time per step of 64 of K, in us, as
-// fitted to 8192 x 4096 products of k = 1024 and 2048 (which take, us, with
-// the tiles in this order: 63 / 71 / 83 and 107 / 119 / 141; k = 256: 31 / 33 /
-// 43; 2048 x 2048 x 1024, which fills the CUs with small tiles only: 23 / 16 /
-// 14; 2048 x 4096 x 4096: 75 / 56 / 67).
+// A product runs in turns of one tile per CU; a turn takes a fixed time (first
+// loads, epilogue) and a time per step of 64 of K, in us, as fitted to bf16
+// products of 256 and more tiles (8192 x 4096, k = 1024: 256 x 256 63, 128 x 256
+// 71, 128 x 128 83; one tile per CU, k = 4096: 128 x 128 32.8, 96 x 128 26.6,
+// 128 x 64 20.7, 96 x 64 17.5, 64 x 64 15.1; two 64 x 64 per CU 25.4).  The
+// small tiles' steps are bound by the LDS: a step's loads and its wavefronts'
+// reads of them, 768 / 624 / 576 / 464 / 384 cycles at 128 bytes each where the
+// MFMAs take 512 / 384 / 256 / 192 / 128, so fewer rows or columns than a larger
+// tile pay only while they fill more CUs.
 struct TurnTime { Tile tile; int bm, bn; double fixed, step; };
-constexpr TurnTime kTurns[] = {{TILE_256X256, 256, 256, 9.0, 1.39},
-                               {TILE_128X256, 128, 256, 5.5, 0.756},
-                               {TILE_128X128, 128, 128, 3.0, 0.456}};
+constexpr TurnTime kTurns[] = {{TILE_256X256, 256, 256, 9.0, 1.39}, {TILE_128X256, 128, 256, 5.5, 0.756},
+                               {TILE_128X128, 128, 128, 3.6, 0.43}, {TILE_96X128, 96, 128, 3.0, 0.35},
+                               {TILE_128X64, 128, 64, 2.4, 0.27},   {TILE_96X64, 96, 64, 1.2, 0.225},
+                               {TILE_64X64, 64, 64, 1.2, 0.18}};
 
-Plan plan_product(int64_t m, int64_t n, int64_t k, int gmode, int64_t groups) {
+Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_t groups) {
   const double steps = std::ceil((double)k / (gmode == BY_K ? (double)groups : 1.0) / kStepK);
   auto tiles = [&](const TurnTime& t) {
     const double cols = (double)((n + t.bn - 1) / t.bn);
@@ -29,32 +33,34 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int gmode, int64_t groups) {
     return (double)((m + t.bm - 1) / t.bm) * cols * (gmode == BY_K ? (double)groups : 1.0);
   };
   Plan p{TILE_128X128, 1, k, 0};
-  double best = -1.0;
-  for (const TurnTime& t : kTurns) {
-    const double cost = std::ceil(tiles(t) / 256.0) * (t.fixed + t.step * steps);
-    if (best < 0.0 || cost < best) {
-      best = cost;
-      p.tile = t.tile;
-    }
-  }
-  if (p.tile != TILE_128X128 || gmode != DENSE) return p;
-  // Split K where that leaves CUs idle: fewer steps against a second launch
-  // (5 us) and the partial sums written and read (4 TB/s).
-  const int64_t t = (int64_t)tiles(kTurns[2]);
+  const TurnTime* chosen = nullptr;
+  double best = 0.0;
   int64_t s = 1;
-  for (int64_t i = 2; i <= 32 && i * t <= 256; i++) {
-    const double cost = kTurns[2].fixed + kTurns[2].step * std::ceil(steps / (double)i) + 5.0 +
-                        (double)i * (double)m * (double)n * 8.0 / 4e6;
-    if (cost < best) {
-      best = cost;
-      s = i;
+  for (const TurnTime& t : kTurns) {
+    if (t.tile > TILE_128X128 && gmode != DENSE) break;
+    if (t.bm == 96 && layout == 2) continue;
+    const double count = tiles(t);
+    for (int64_t i = 1; i <= 32; i++) {
+      // K in i parts where that leaves no CU a second tile: fewer steps against
+      // a second launch (4.5 us) and the partial sums written and read (4 TB/s)
+      if (i > 1 && (t.bn > 128 || gmode != DENSE || (double)i * count > 256.0)) break;
+      double cost = std::ceil((double)i * count / 256.0) * (t.fixed + t.step * std::ceil(steps / (double)i));
+      if (i > 1) cost += 4.5 + (double)i * (double)m * (double)n * 8.0 / 4e6;
+      if (!chosen || cost < best) {
+        best = cost;
+        chosen = &t;
+        s = i;
+      }
     }
   }
+  p.tile = chosen->tile;
   if (s > 1) {
     p.k_part = ((k + s - 1) / s + kStepK - 1) / kStepK * kStepK;
     p.splits = (int)((k + p.k_part - 1) / p.k_part);
-    if (p.splits > 1)
-      p.partial_bytes = (size_t)p.splits * ((m + 127) / 128 * 128) * ((n + 127) / 128 * 128) * sizeof(float);
+    if (p.splits > 1) {
+      auto whole = [](int64_t v, int64_t by) { return (v + by - 1) / by * by; };
+      p.partial_bytes = (size_t)p.splits * whole(m, chosen->bm) * whole(n, chosen->bn) * sizeof(float);
+    }
   }
   return p;
 }
@@ -300,11 +306,12 @@ struct ForwardLayout {
   Plan plan;
   ForwardLayout(int64_t m, int64_t k, int64_t n, int64_t groups) {
     Parts p;
-    plan = plan_product(m, n, k, groups ? BY_ROWS : DENSE, groups);
-    const bool skinny = !groups && m <= kSkinnyRows, ragged = k % 8 != 0 && !skinny;
+    const bool skinny = !groups && m <= kSkinnyRows;
+    plan = skinny ? Plan{} : plan_product(m, n, k, 0, groups ? BY_ROWS : DENSE, groups);
+    const bool ragged = k % 8 != 0 && !skinny;
     x8 = p.take(ragged ? (size_t)m * pad8(k) * 2 : 0);
     w8 = p.take(ragged ? (size_t)std::max<int64_t>(groups, 1) * n * pad8(k) * 2 : 0);
-    partial = p.take(skinny ? 0 : plan.partial_bytes);
+    partial = p.take(plan.partial_bytes);
     total = p.used;
   }
 };
@@ -314,8 +321,8 @@ struct GradLayout {
   Plan dx, dw;
   GradLayout(int64_t m, int64_t k, int64_t n, int64_t groups) {
     Parts p;
-    dx = plan_product(m, k, n, groups ? BY_ROWS : DENSE, groups);
-    dw = plan_product(n, k, m, groups ? BY_K : DENSE, groups);
+    dx = plan_product(m, k, n, 1, groups ? BY_ROWS : DENSE, groups);
+    dw = plan_product(n, k, m, 2, groups ? BY_K : DENSE, groups);
     dz = p.take((size_t)m * pad8(n) * 2);
     sums = p.take((size_t)dz_tiles(m, groups) * n * sizeof(float));
     x8 = p.take(k % 8 ? (size_t)m * pad8(k) * 2 : 0);

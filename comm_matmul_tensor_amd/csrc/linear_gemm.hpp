@@ -14,14 +14,17 @@
 // per SIMD (one with the 128 x 128 tile) with interleaved MFMAs, LDS reads and
 // loads; the launcher picks the tile (plan_product).
 //
-// Bound by the MFMAs at the clock the card holds under them: 8192 x 8192 x 8192
+// Large products are bound by the MFMAs at the clock the card holds under them: 8192 x 8192 x 8192
 // 767 us, 1.43 PFLOP/s (as the vendor library's product on the same card);
 // 4096 x 7168 x 4096 with bias, gelu and z 204 us (1.18); its gradients' two
 // products 174 and 182 us (1.38, 1.32).  Measured and left out: loads ahead of
 // time that only bring lines into the L2 (4 bytes per line, 1 to 6 steps
 // ahead; by every workgroup or by one per band) 5 to 40 % slower; K walked from
 // a step set by the tile, no change or 10 % slower; 256 x 224 tiles, which fill
-// the CUs better at n = 7168, within 5 % either way.
+// the CUs better at n = 7168, within 5 % either way.  Products of one tile per
+// CU are bound by the LDS, which a step's loads and fragment reads pass: 517 x
+// 1792 x 4096 13.5 us (15.0 in 128 x 128 tiles), 256 x 4096 x 4096 14.8 (22.3),
+// 1024 x 1024 x 1024 8.7 (10.4).
 //
 // Groups of rows (experts): the tile's rows come from one group's range of
 // rows, found from the ranges on the device (find_tile), with that group's
@@ -258,12 +261,12 @@ template <int BM, int BN, int NT>
 __device__ __forceinline__ void store_tile(const uint16_t* h0, const uint16_t* h1, uint16_t* c, int64_t m0,
                                            int64_t m_end, int64_t n0, int64_t n) {
   constexpr int kRow = BN / 8, kPitch = BN + 8;
-  static_assert(BM * kRow % NT == 0, "whole turns");
+  constexpr bool kWhole = BM * kRow % NT == 0;
   auto src_of = [&](int row, int col) {
     return (row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col;
   };
   const bool vec = n % 8 == 0;
-  if (vec && m0 + BM <= m_end && n0 + BN <= n) {  // the tile lies inside C: no tests between the stores
+  if (kWhole && vec && m0 + BM <= m_end && n0 + BN <= n) {  // the tile lies inside C: no tests between the stores
 #pragma unroll
     for (int it = 0; it < BM * kRow / NT; it++) {
       const int s = (int)threadIdx.x + it * NT, row = s / kRow, col = (s % kRow) * 8;
@@ -390,9 +393,20 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
   constexpr int NA = Loader<BM, AK, NT>::kN, ND = NA + Loader<BN, BK, NT>::kN, NM = FM * FN;
   u32x4 fa[FM - 1], la0, la1, fb0[FN], fb1[FN];
-  // reads of B: kPerRow after each of rows 1, 2, ..., kGap MFMAs apart
+  // reads of B: kPerRow in each of rows 1, 2, ..., kGap MFMAs apart; with two
+  // rows or columns of MFMAs spread over the rows after the first
   constexpr int kPerRow = (FN + FM - 2) / (FM - 1) < 2 ? 2 : (FN + FM - 2) / (FM - 1), kGap = (FN - 1) / kPerRow;
-  static_assert(kGap >= 1 && kPerRow * kGap < FN && kPerRow * (FM - 1) >= FN, "room for B's reads");
+  static_assert(kGap < 1 || (kPerRow * kGap < FN && kPerRow * (FM - 1) >= FN), "room for B's reads");
+  auto read_of_b = [](int q) {  // the fragment read after MFMA q, or FN
+    if constexpr (kGap >= 1) {
+      const int i = q / FN, j = q % FN;
+      return i > 0 && j > 0 && j % kGap == 0 && j / kGap <= kPerRow ? kPerRow * (i - 1) + j / kGap - 1 : FN;
+    } else {
+      for (int f = 0; f < FN; f++)
+        if (FN + f * (NM - FN) / FN == q) return f;
+      return FN;
+    }
+  };
   auto half = [&](const u32x4& last, u32x4& next_last, const u32x4(&fb)[FN], u32x4(&nb)[FN], auto LOAD_, uint8_t* to,
                   int kt_load, const uint8_t* from, int kk) {
     constexpr bool LOAD = decltype(LOAD_)::value;
@@ -406,10 +420,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
         acc[i][j] = mfma16<DT>(fb[j], i < FM - 1 ? fa[i < FM - 1 ? i : 0] : last, acc[i][j]);
         if (i > 0 && j == 0) fa[i - 1] = ra.read_one(from, kk, i - 1);
         if (i == 0 && j == FN - 1) next_last = ra.read_one(from, kk, FM - 1);
-        if (i > 0 && j > 0 && j % kGap == 0 && j / kGap <= kPerRow) {
-          const int f = kPerRow * (i - 1) + j / kGap - 1;
-          if (f < FN) nb[f] = rb.read_one(from + kATile, kk, f);
-        }
+        if (const int f = read_of_b(q); f < FN) nb[f] = rb.read_one(from + kATile, kk, f);
         if constexpr (LOAD) {
 #pragma unroll
           for (int d = 0; d < ND; d++)
@@ -439,7 +450,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
   };
   // The residual's values of this lane.  Where a wavefront has registers for
   // them they are loaded before the main loop, which hides their latency
-  // (517 x 1792 x 4096 in fp16: 17.9 -> 17.4 us; 15.8 without a residual).
+  // (517 x 1792 x 4096 in fp16 by 128 x 128 tiles: 17.9 -> 17.4 us).
   const uint16_t* residual = static_cast<const uint16_t*>(p.residual);
   const bool quads = p.n % 4 == 0;
   const int64_t col0 = n0 + wn * WN + 4 * (lane / 16);  // this lane's first column

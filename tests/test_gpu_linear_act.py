@@ -114,6 +114,18 @@ def test_forward_groups(mc2, m, offsets, k, n):
     run_forward(mc2, 22, m, k, n, "f16", "none", False, False, offsets, keep_z=False)
 
 
+# outputs of 193 to 256 tiles of 96 x 64, 128 x 64 and 96 x 128, with partial ones at both edges; 64 x 64 whole
+# and with K in parts
+MIDDLE = [(381, 150, 4090), (509, 77, 4091), (761, 456, 4088), (250, 136, 4088), (70, 2056, 1030), (512, 512, 4096)]
+
+
+@pytest.mark.parametrize("m,k,n", MIDDLE)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_forward_middle_tiles(mc2, m, k, n, dtype):
+    print(f"linear m={m} k={k} n={n} {dtype}", flush=True)
+    run_forward(mc2, 26, m, k, n, dtype, "gelu_tanh", True, True)
+
+
 def many_groups(m, groups):
     """Ranges of 0 to 60 rows, every fifth one empty, one end out of order, rows left over."""
     g = torch.Generator().manual_seed(groups)
@@ -197,6 +209,14 @@ def test_grad_large_tiles(mc2, m, k, n):
     """Large and small outputs of either product: every tile, and a split contraction."""
     print(f"linear_grad m={m} k={k} n={n}", flush=True)
     run_grad(mc2, 32, m, k, n, "bf16", "silu")
+
+
+@pytest.mark.parametrize("m,n,k", MIDDLE)
+def test_grad_middle_tiles(mc2, m, n, k):
+    """dx (m, k), and dw (n, k) by as many rows of it, with tiles under 128 x 128."""
+    print(f"linear_grad m={m} k={k} n={n}", flush=True)
+    run_grad(mc2, 38, m, k, n, "bf16", "silu")
+    run_grad(mc2, 39, n, k, m, "f16", "none")
 
 
 @pytest.mark.parametrize("m,offsets", GROUPS)
