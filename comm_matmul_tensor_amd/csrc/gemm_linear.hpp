@@ -64,14 +64,14 @@ hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
 
 template <int DT, bool AK, bool BK, int GMODE>
 hipError_t launch_layout(const Product& p, const Plan& plan, hipStream_t s) {
-  if constexpr (GMODE == DENSE) {
-    if constexpr (AK) {
-      if (plan.tile == TILE_96X128) return launch_tile<DT, 96, 128, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
-      if (plan.tile == TILE_96X64) return launch_tile<DT, 96, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
-    }
-    if (plan.tile == TILE_128X64) return launch_tile<DT, 128, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
-    if (plan.tile == TILE_64X64) return launch_tile<DT, 64, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+  if constexpr (AK) {
+    if (plan.tile == TILE_96X128) return launch_tile<DT, 96, 128, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+    if (plan.tile == TILE_96X64) return launch_tile<DT, 96, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
   }
+  if constexpr (GMODE == DENSE)
+    if (plan.tile == TILE_128X64) return launch_tile<DT, 128, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+  if constexpr (GMODE != BY_K)
+    if (plan.tile == TILE_64X64) return launch_tile<DT, 64, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
   switch (plan.tile) {
     case TILE_256X256: return launch_tile<DT, 256, 256, 2, 4, 2, AK, BK, GMODE>(p, plan, s);
     case TILE_128X256: return launch_tile<DT, 128, 256, 2, 4, 3, AK, BK, GMODE>(p, plan, s);

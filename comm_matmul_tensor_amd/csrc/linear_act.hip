@@ -17,7 +17,10 @@ namespace lin {
 // small tiles' steps are bound by the LDS: a step's loads and its wavefronts'
 // reads of them, 768 / 624 / 576 / 464 / 384 cycles at 128 bytes each where the
 // MFMAs take 512 / 384 / 256 / 192 / 128, so fewer rows or columns than a larger
-// tile pay only while they fill more CUs.
+// tile pay only while they fill more CUs.  Groups of rows are taken as equal,
+// with half a tile more than their rows fill each, one tile at least (64
+// matrices of 4096 x 1792, 8 rows in all: 64 x 64 22.7 us, 128 x 128 32.9; 8
+// matrices, 1024 rows: 96 x 128 35.4, 128 x 128 44.3, 128 x 256 60.5).
 struct TurnTime { Tile tile; int bm, bn; double fixed, step; };
 constexpr TurnTime kTurns[] = {{TILE_256X256, 256, 256, 9.0, 1.39}, {TILE_128X256, 128, 256, 5.5, 0.756},
                                {TILE_128X128, 128, 128, 3.6, 0.43}, {TILE_96X128, 96, 128, 3.0, 0.35},
@@ -28,8 +31,10 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
   const double steps = std::ceil((double)k / (gmode == BY_K ? (double)groups : 1.0) / kStepK);
   auto tiles = [&](const TurnTime& t) {
     const double cols = (double)((n + t.bn - 1) / t.bn);
-    // groups of rows: each group's last tile taken as half a tile
-    if (gmode == BY_ROWS) return ((double)m / t.bm + 0.5 * (double)groups) * cols;
+    if (gmode == BY_ROWS) {
+      const double some = (double)std::min(m, groups);  // groups with rows, at most
+      return std::max(some, (double)m / t.bm + 0.5 * some) * cols;
+    }
     return (double)((m + t.bm - 1) / t.bm) * cols * (gmode == BY_K ? (double)groups : 1.0);
   };
   Plan p{TILE_128X128, 1, k, 0};
@@ -37,8 +42,8 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
   double best = 0.0;
   int64_t s = 1;
   for (const TurnTime& t : kTurns) {
-    if (t.tile > TILE_128X128 && gmode != DENSE) break;
-    if (t.bm == 96 && layout == 2) continue;
+    if (t.tile > TILE_128X128 && gmode == BY_K) break;
+    if ((t.bm == 96 && layout == 2) || (t.tile == TILE_128X64 && gmode == BY_ROWS)) continue;
     const double count = tiles(t);
     for (int64_t i = 1; i <= 32; i++) {
       // K in i parts where that leaves no CU a second tile: fewer steps against

@@ -9,8 +9,8 @@ namespace lin {
 // The tiles: 256 x 256 in two LDS stages, 128 x 256 in three, 128 x 128 in
 // four.  A larger tile reads less per product; a smaller one fills the CUs
 // better, and its deeper ring of stages covers more of the latency.  The
-// tiles under 128 x 128 (four stages) are for dense products of few tiles;
-// those of 96 rows need a K-contiguous A.
+// tiles under 128 x 128 (four stages) are for products of few tiles and for
+// groups of few rows; those of 96 rows need a K-contiguous A.
 enum Tile : int { TILE_256X256, TILE_128X256, TILE_128X128, TILE_96X128, TILE_128X64, TILE_96X64, TILE_64X64 };
 
 // Tile and split of a product, from its sizes alone (the workspace's size
