@@ -61,6 +61,24 @@ def test_permute(mc2, tokens, top, experts, skew):
     assert torch.equal(out.cpu(), want)
 
 
+# choices on both sides of 256 and of 1024, many per token, more experts than choices
+FEW = [(64, 4, 160), (257, 1, 4096), (128, 8, 32), (205, 5, 64), (2, 500, 3), (1, 64, 64), (1024, 1, 963)]
+
+
+@pytest.mark.parametrize("tokens,top,experts", FEW)
+@pytest.mark.parametrize("h", [7, 264, 2056])
+def test_permute_few(mc2, tokens, top, experts, h):
+    print(f"permute tokens={tokens} top={top} experts={experts} h={h}", flush=True)
+    x, ids = rand(30, tokens, h), make_ids(31 + tokens, tokens, top, experts, drop=0.2)
+    out, row_map, offsets = mc2.mc2_moe_permute(x.cuda(), ids.cuda(), experts)
+    want_map, want_offsets, order = plain_map(ids, experts)
+    assert torch.equal(row_map.cpu(), want_map)
+    assert torch.equal(offsets.cpu(), want_offsets)
+    want = torch.zeros((tokens * top, h), dtype=x.dtype)
+    want[:len(order)] = x[torch.tensor(order, dtype=torch.long) // top]
+    assert torch.equal(out.cpu(), want)
+
+
 @pytest.mark.parametrize("h", [1, 5, 8, 63, 64, 1000, 2048, 2056, 4096, 7168])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_permute_widths(mc2, h, dtype):
