@@ -31,7 +31,9 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 // Eight 16-bit elements of a row of h from column c (a multiple of 8), zeros
 // past its end.  VEC: h is a multiple of 8, so the chunk is whole and its
 // address 16-byte aligned; otherwise a whole chunk is one load of 2-byte
-// alignment and a partial one goes element by element.
+// alignment, and a row's last, partial one is the load of its last 8 elements
+// shifted into place (element by element, 8 times a load's latency, only in
+// rows shorter than that).
 template <bool VEC>
 __device__ __forceinline__ u32x4 load_chunk(const uint16_t* row, int64_t c, int64_t h) {
   if constexpr (VEC) {
@@ -40,6 +42,12 @@ __device__ __forceinline__ u32x4 load_chunk(const uint16_t* row, int64_t c, int6
     u32x4 v = {0u, 0u, 0u, 0u};
     if (c + 8 <= h) {
       __builtin_memcpy(&v, row + c, 16);
+    } else if (h >= 8) {
+      if (c < h) {
+        unsigned __int128 t;
+        __builtin_memcpy(&t, row + h - 8, 16);
+        v = __builtin_bit_cast(u32x4, t >> (16 * (int)(c + 8 - h)));
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; e++)

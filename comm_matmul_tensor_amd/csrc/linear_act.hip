@@ -77,31 +77,40 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------- ragged rows
 // dst (rows, ld) = src (rows, k) with zeros in columns k .. ld - 1, for up to
-// two matrices in one launch.
+// two matrices in one launch; tpr threads per row.
 struct PadArgs {
   const uint16_t* src[2];
   uint16_t* dst[2];
   int64_t rows[2];
   int64_t k, ld;
+  int tpr;
 };
 __global__ __launch_bounds__(256) void pad_rows(PadArgs a) {
-  const int64_t chunks = a.ld / 8, first = a.rows[0] * chunks, all = first + a.rows[1] * chunks;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-    const int which = i >= first;
-    const int64_t j = which ? i - first : i, row = j / chunks, c = j % chunks * 8;
-    *reinterpret_cast<u32x4*>(a.dst[which] + row * a.ld + c) = load_chunk<false>(a.src[which] + row * a.k, c, a.k);
+  const int per = 256 / a.tpr;
+  for (int64_t i = (int64_t)blockIdx.x * per + threadIdx.x / a.tpr; i < a.rows[0] + a.rows[1];
+       i += (int64_t)gridDim.x * per) {
+    const int which = i >= a.rows[0];
+    const int64_t row = which ? i - a.rows[0] : i;
+    const uint16_t* src = a.src[which] + row * a.k;
+    uint16_t* dst = a.dst[which] + row * a.ld;
+#pragma unroll 4
+    for (int64_t c = 8 * (int64_t)(threadIdx.x % a.tpr); c < a.ld; c += 8 * a.tpr)
+      *reinterpret_cast<u32x4*>(dst + c) = load_chunk<false>(src, c, a.k);
   }
 }
 hipError_t launch_pad_rows(const void* s0, int64_t rows0, void* d0, const void* s1, int64_t rows1, void* d1, int64_t k,
                            hipStream_t s) {
+  if (rows0 + rows1 == 0) return hipSuccess;
+  int tpr = 1;
+  while (tpr < 256 && 8 * tpr < k) tpr *= 2;
   const PadArgs a{{static_cast<const uint16_t*>(s0), static_cast<const uint16_t*>(s1)},
                   {static_cast<uint16_t*>(d0), static_cast<uint16_t*>(d1)},
                   {rows0, rows1},
                   k,
-                  pad8(k)};
-  const int64_t chunks = (rows0 + rows1) * (pad8(k) / 8);
-  if (chunks == 0) return hipSuccess;
-  pad_rows<<<(unsigned)std::min<int64_t>((chunks + 255) / 256, 256 * 16), 256, 0, s>>>(a);
+                  pad8(k),
+                  tpr};
+  const int64_t blocks = (rows0 + rows1 + 256 / tpr - 1) / (256 / tpr);
+  pad_rows<<<(unsigned)std::min<int64_t>(blocks, 256 * 16), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

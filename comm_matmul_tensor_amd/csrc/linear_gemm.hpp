@@ -278,14 +278,9 @@ __device__ __forceinline__ void store_tile(const uint16_t* h0, const uint16_t* h
     const int row = s / kRow, col = (s % kRow) * 8;
     const int64_t gr = m0 + row, gc = n0 + col;
     if (gr >= m_end || gc >= n) continue;
-    uint16_t* dst = c + gr * n + gc;
-    const uint16_t* src = src_of(row, col);
-    if (vec) {
-      store_out16(dst, *reinterpret_cast<const u32x4*>(src));
-    } else {
-      for (int e = 0; e < 8; e++)
-        if (gc + e < n) dst[e] = src[e];
-    }
+    const u32x4 v = *reinterpret_cast<const u32x4*>(src_of(row, col));
+    if (vec) store_chunk<true, true>(c + gr * n, gc, n, v);
+    else store_chunk<false, true>(c + gr * n, gc, n, v);
   }
 }
 
@@ -296,9 +291,11 @@ __device__ __forceinline__ u32x2 load4(const uint16_t* p, int64_t left, bool qua
   u32x2 v = {0u, 0u};
   if (quads) {
     if (left > 0) v = *reinterpret_cast<const u32x2*>(p);
+  } else if (left >= 4) {
+    __builtin_memcpy(&v, p, 8);
   } else {
 #pragma unroll
-    for (int r = 0; r < 4; r++)
+    for (int r = 0; r < 3; r++)
       if (r < left) v[r / 2] |= (uint32_t)p[r] << (16 * (r & 1));
   }
   return v;
