@@ -49,8 +49,10 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
       // K in i parts where that leaves no CU a second tile: fewer steps against
       // a second launch (4.5 us) and the partial sums written and read (4 TB/s)
       if (i > 1 && (t.bn > 128 || gmode != DENSE || (double)i * count > 256.0)) break;
-      double cost = std::ceil((double)i * count / 256.0) * (t.fixed + t.step * std::ceil(steps / (double)i));
-      if (i > 1) cost += 4.5 + (double)i * (double)m * (double)n * 8.0 / 4e6;
+      const double join = i > 1 ? 4.5 + (double)i * (double)m * (double)n * 8.0 / 4e6 : 0.0;
+      if (i > 1 && t.fixed + join >= best) break;  // nor would more parts
+      const double cost =
+          std::ceil((double)i * count / 256.0) * (t.fixed + t.step * std::ceil(steps / (double)i)) + join;
       if (!chosen || cost < best) {
         best = cost;
         chosen = &t;
