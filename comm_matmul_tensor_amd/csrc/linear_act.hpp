@@ -51,22 +51,26 @@ __device__ __forceinline__ float act_of(float z) {
   return z;
 }
 
+// The slopes tend to 1 and 0 where a term z (1 - p) p would be inf * 0, so z is
+// taken within +-1e4 there, where that term has long been 0.  An infinite z is
+// no rare input: a pre-activation past fp16's range is saved as one.  (The
+// clamp drops a NaN, p keeps it.)
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  const float zc = __builtin_amdgcn_fmed3f(z, -1e4f, 1e4f);
   if constexpr (ACT == ACT_GELU) {
     float e;
     const float p = normal_cdf(z, e);
-    return __builtin_fmaf(z * 0.39894228040143267794f, e, p);
+    return __builtin_fmaf(zc * 0.39894228040143267794f, e, p);
   }
   if constexpr (ACT == ACT_GELU_TANH) {
-    // (z^2 kept finite: its product with the 0 of 1 - p is 0)
-    const float z2 = fminf(z * z, 1e30f), p = sigmoid(z * __builtin_fmaf(kTanhB, z2, kTanhA));
-    return __builtin_fmaf(z * p * (1.0f - p), __builtin_fmaf(3.0f * kTanhB, z2, kTanhA), p);
+    const float z2 = zc * zc, p = sigmoid(z * __builtin_fmaf(kTanhB, z2, kTanhA));
+    return __builtin_fmaf(zc * p * (1.0f - p), __builtin_fmaf(3.0f * kTanhB, z2, kTanhA), p);
   }
   if constexpr (ACT == ACT_SILU) {
     const float p = sigmoid(z);
-    return __builtin_fmaf(z * p, 1.0f - p, p);
+    return __builtin_fmaf(zc * p, 1.0f - p, p);
   }
   return 1.0f;
 }
