@@ -5,7 +5,8 @@
 token's chosen experts, weighted by its router.  Both return the new residual
 stream, so that blocks chain with the norm's own addition, and train through
 the autograd functions here, whose every step is a libmc2 call: the only torch
-operations are views and the router's choice (a product and a top-k).
+operations are views and the router's choice (a top-k and a softmax).  Their
+gradients cannot be differentiated again: a second backward through them raises.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ from typing import Optional
 
 import torch
 
+from ._autograd import first_order
 from .layer import (MC2_ACT_GELU, MC2_ACT_NONE, MC2_ACT_SILU, mc2_add_rms_norm, mc2_add_rms_norm_grad, mc2_linear_act,
                     mc2_linear_act_grad, mc2_moe_permute, mc2_moe_unpermute, mc2_moe_unpermute_grad)
 
@@ -33,6 +35,7 @@ class AddRMSNormFunction(torch.autograd.Function):
         return out, s if ctx.has_residual else s.view_as(s)
 
     @staticmethod
+    @first_order
     def backward(ctx, dout, dsum):
         s, weight, rstd = ctx.saved_tensors
         if dout is None:
@@ -54,6 +57,7 @@ class LinearActFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         x, w, z, group_offsets = ctx.saved_tensors
         dout = dout.contiguous()
@@ -74,6 +78,7 @@ class PermuteFunction(torch.autograd.Function):
         return out, row_map, offsets
 
     @staticmethod
+    @first_order
     def backward(ctx, dout, _map, _offsets):
         (row_map,) = ctx.saved_tensors
         return mc2_moe_unpermute(dout.contiguous(), row_map), None, None
@@ -88,6 +93,7 @@ class UnpermuteFunction(torch.autograd.Function):
         return mc2_moe_unpermute(y, row_map, weights)
 
     @staticmethod
+    @first_order
     def backward(ctx, dout):
         y, row_map, weights = ctx.saved_tensors
         dy, dweights = mc2_moe_unpermute_grad(dout.contiguous(), y, row_map, weights,
