@@ -22,7 +22,8 @@ run every rank's share: each step is a libmc2 call (the GEMMs, the gathers,
 the reduce-scatter sums, the bias and its gradient all run in its HIP
 kernels).  The only torch operations are allocations, views and, for a
 sequence dimension other than 0, the permute-and-copy of the dimension move
-(data movement, as in the listing).
+(data movement, as in the listing).  The gradients cannot be differentiated
+again: a second backward through them raises.
 """
 from __future__ import annotations
 
@@ -32,6 +33,7 @@ import torch
 
 from . import (mc2_allgather_matmul, mc2_bias_grad, mc2_matmul_grad_input, mc2_matmul_grad_weight,
                mc2_matmul_reduce_scatter)
+from ._autograd import first_order
 
 __all__ = ["AllGatherMatmulFunction", "MatmulReduceScatterFunction", "MC2Linear", "move_dim_to_front",
            "move_front_to_dim", "normalize_sequence_dim"]
@@ -85,6 +87,7 @@ class AllGatherMatmulFunction(torch.autograd.Function):
         return tuple(outs)
 
     @staticmethod
+    @first_order
     def backward(ctx, *grad_outs):
         r = ctx.r
         gathered, *ws = ctx.saved_tensors
@@ -141,6 +144,7 @@ class MatmulReduceScatterFunction(torch.autograd.Function):
         return tuple(outs)
 
     @staticmethod
+    @first_order
     def backward(ctx, *grad_outs):
         r = ctx.r
         saved = ctx.saved_tensors
