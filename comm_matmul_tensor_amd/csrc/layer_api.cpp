@@ -227,7 +227,7 @@ mc2_status mc2_moe_unpermute_grad(const void* dout, const void* y, const int32_t
                                   float* dweights, void* stream) {
   clear_error();
   mc2_status s = check_moe_unpermute_grad(dout, y, row_map, weights, tokens, top, h, rows, dtype, dy, dweights);
-  if (s != MC2_OK) return s;
+  if (s != MC2_OK || ((rows == 0 || !dy) && (tokens == 0 || !dweights))) return s;  // (or nothing to write)
   int dev;
   if ((s = current_device(&dev)) != MC2_OK) return s;
   UnpermuteArgs a{};

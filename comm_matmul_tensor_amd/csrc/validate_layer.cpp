@@ -181,7 +181,7 @@ mc2_status check_moe_unpermute_grad(const void* dout, const void* y, const void*
                                     const void* dy, const void* dweights) {
   const char* who = "moe_unpermute_grad";
   MC2_TRY(check_unpermute_sizes(who, tokens, top, h, rows, dtype));
-  if (!dy && !dweights) return fail(MC2_ERR_NULL, "moe_unpermute_grad: dy or dweights is required");
+  if (rows > 0 && !dy && !dweights) return fail(MC2_ERR_NULL, "moe_unpermute_grad: dy or dweights is required");
   if (tokens > 0) MC2_TRY(required(who, {dout, row_map}, "dout and row_map"));
   if (dweights && tokens > 0 && rows > 0 && !y)
     return fail(MC2_ERR_NULL, "moe_unpermute_grad: dweights needs y");

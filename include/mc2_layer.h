@@ -151,7 +151,7 @@ mc2_status mc2_moe_unpermute(const void* y, const int32_t* row_map, const float*
  * row_map is one mc2_moe_permute gave: with c kept choices it names each of
  * the rows 0 .. c - 1 once, and dy's rows c .. rows - 1 become 0.  weights
  * NULL: all 1.  dweights (tokens, top) fp32 or NULL, y (rows, h) needed only
- * for it, dy (rows, h) or NULL.
+ * for it, dy (rows, h) or NULL; with rows one of the two is required.
  */
 mc2_status mc2_moe_unpermute_grad(const void* dout, const void* y, const int32_t* row_map, const float* weights,
                                   int64_t tokens, int64_t top, int64_t h, int64_t rows, mc2_dtype dtype, void* dy,
