@@ -22,6 +22,13 @@ __all__ = ["AddRMSNormFunction", "LinearActFunction", "PermuteFunction", "Unperm
            "ExpertsFeedForward"]
 
 
+def _ready(grad):
+    """An incoming gradient as the library takes it: contiguous and 16-byte aligned (one that is a part of a
+    concatenation's may start anywhere)."""
+    grad = grad.contiguous()
+    return grad.clone() if grad.data_ptr() % 16 else grad
+
+
 class AddRMSNormFunction(torch.autograd.Function):
     """(norm(x + residual) * weight, x + residual)."""
 
@@ -40,8 +47,7 @@ class AddRMSNormFunction(torch.autograd.Function):
         s, weight, rstd = ctx.saved_tensors
         if dout is None:
             return dsum, dsum if ctx.has_residual else None, None, None
-        dx, dweight = mc2_add_rms_norm_grad(dout.contiguous(), s, weight, rstd,
-                                            None if dsum is None else dsum.contiguous())
+        dx, dweight = mc2_add_rms_norm_grad(_ready(dout), s, weight, rstd, None if dsum is None else _ready(dsum))
         return dx, dx if ctx.has_residual else None, dweight, None
 
 
@@ -60,7 +66,7 @@ class LinearActFunction(torch.autograd.Function):
     @first_order
     def backward(ctx, dout):
         x, w, z, group_offsets = ctx.saved_tensors
-        dout = dout.contiguous()
+        dout = _ready(dout)
         dx, dw, dbias = mc2_linear_act_grad(dout, x, w, z, act=ctx.act, group_offsets=group_offsets,
                                             need_dx=ctx.needs_input_grad[0], need_dw=ctx.needs_input_grad[1],
                                             need_dbias=ctx.has_bias and ctx.needs_input_grad[2])
@@ -81,7 +87,7 @@ class PermuteFunction(torch.autograd.Function):
     @first_order
     def backward(ctx, dout, _map, _offsets):
         (row_map,) = ctx.saved_tensors
-        return mc2_moe_unpermute(dout.contiguous(), row_map), None, None
+        return mc2_moe_unpermute(_ready(dout), row_map), None, None
 
 
 class UnpermuteFunction(torch.autograd.Function):
@@ -96,7 +102,7 @@ class UnpermuteFunction(torch.autograd.Function):
     @first_order
     def backward(ctx, dout):
         y, row_map, weights = ctx.saved_tensors
-        dy, dweights = mc2_moe_unpermute_grad(dout.contiguous(), y, row_map, weights,
+        dy, dweights = mc2_moe_unpermute_grad(_ready(dout), y, row_map, weights,
                                               need_dweights=ctx.needs_input_grad[2])
         return dy, None, dweights
 

@@ -113,3 +113,30 @@ def test_second_derivatives_are_refused(name, loss):
         with pytest.raises(RuntimeError, match="second derivatives"):
             (fn(*ts)[0].sum() + g.square().sum()).backward(retain_graph=True)
 
+
+
+def aligned(t):
+    return t is None or (t.is_contiguous() and t.data_ptr() % 16 == 0)
+
+
+@pytest.mark.parametrize("name", sorted(calls()))
+def test_gradients_arrive_aligned(name, monkeypatch):
+    """A gradient may come in as a view at any address, as of a part of a concatenation: the library's calls get it
+    contiguous and 16-byte aligned, which they require."""
+    torch.manual_seed(4)
+    seen = []
+    for fn in (linear_act_grad, add_rms_norm_grad, moe_unpermute_grad, moe_unpermute):
+        def checked(*args, _fn=fn, **kwargs):
+            seen.append(all(aligned(a) for a in args if isinstance(a, torch.Tensor)))
+            return _fn(*args, **kwargs)
+        monkeypatch.setattr(ff, "mc2_" + fn.__name__, checked)
+    fn, ts = calls()[name]
+    outs = fn(*ts)
+    for out in outs if isinstance(outs, tuple) else (outs,):
+        wide = torch.randn((out.numel() + 1,), dtype=torch.float64)
+        for grad in (wide[1:].view(out.shape), wide[1:].view(out.shape).t().contiguous().t(), torch.ones(()).double().expand(out.shape)):
+            got = torch.autograd.grad(out, ts, grad, retain_graph=True, allow_unused=True)
+            want = torch.autograd.grad(out, ts, grad.contiguous().clone(), retain_graph=True, allow_unused=True)
+            for g, p in zip(got, want):
+                assert (g is None) == (p is None) and (g is None or torch.equal(g, p))
+    assert all(seen)
