@@ -7,6 +7,7 @@
 #include "api_internal.hpp"
 #include "layer_kernels.hpp"
 #include "mc2_layer.h"
+#include "testing.h"
 #include "validate_layer.hpp"
 
 namespace mc2 {
@@ -243,6 +244,17 @@ mc2_status mc2_moe_unpermute_grad(const void* dout, const void* y, const int32_t
   a.dy = dy;
   a.dweights = dweights;
   return launched(launch_moe_unpermute_grad(a, static_cast<hipStream_t>(stream)), "moe_unpermute_grad launch");
+}
+
+mc2_status mc2_testing_linear_plan(int product, int64_t m, int64_t k, int64_t n, int64_t groups, int* tile,
+                                   int* splits) {
+  clear_error();
+  if (!tile || !splits) return fail(MC2_ERR_NULL, "testing_linear_plan: tile and splits are required");
+  if (product < 0 || product > 2) return fail(MC2_ERR_UNSUPPORTED, "testing_linear_plan: no such product");
+  mc2_status s = check_linear_sizes("testing_linear_plan", m, k, n, groups);
+  if (s != MC2_OK) return s;
+  linear_act_plan(product, m, k, n, groups, tile, splits);
+  return MC2_OK;
 }
 
 }  // extern "C"

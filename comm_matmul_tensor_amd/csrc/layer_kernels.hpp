@@ -52,6 +52,8 @@ struct LinearGradArgs {
   void* workspace;
 };
 size_t linear_act_grad_workspace(int64_t m, int64_t k, int64_t n, int64_t groups);
+// The tile and the parts of K of a call's product (testing.h).
+void linear_act_plan(int product, int64_t m, int64_t k, int64_t n, int64_t groups, int* tile, int* splits);
 hipError_t launch_linear_act_grad(const LinearGradArgs& a, hipStream_t s);
 
 // ---- K12: tokens' rows by expert and back

@@ -177,15 +177,20 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(Product p) {
 
 constexpr int64_t kSkinnyRows = 32;
 
+// Wavefronts of a workgroup: 4 where the columns make 1.5 to 4 workgroups per
+// CU, 16 where they make fewer (to cover HBM's latency) or more (fewer rows
+// of w read at a time).  One row, us with 4 / 16: 4096 x 7168 12.7 / 13.4,
+// 7168 x 4096 14.2 / 11.5, 8192 x 28672 92 / 84 (470 MB, 5.6 TB/s).
+int skinny_waves(int64_t n) {
+  const int64_t blocks = (n + 15) / 16;
+  return blocks >= 384 && blocks < 1024 ? 4 : 16;
+}
+
 template <int DT, int MF>
 hipError_t launch_skinny(const Product& p, hipStream_t s) {
   const unsigned blocks = (unsigned)((p.n + 15) / 16);
   const bool vec = p.k % 8 == 0;
-  // 4 wavefronts a workgroup where the columns make 1.5 to 4 workgroups per
-  // CU, 16 where they make fewer (to cover HBM's latency) or more (fewer rows
-  // of w read at a time).  One row, us with 4 / 16: 4096 x 7168 12.7 / 13.4,
-  // 7168 x 4096 14.2 / 11.5, 8192 x 28672 92 / 84 (470 MB, 5.6 TB/s).
-  if (blocks >= 384 && blocks < 1024) {
+  if (skinny_waves(p.n) == 4) {
     if (vec) skinny_kernel<DT, MF, 4, true><<<blocks, 256, 0, s>>>(p);
     else skinny_kernel<DT, MF, 4, false><<<blocks, 256, 0, s>>>(p);
   } else {
@@ -443,6 +448,23 @@ hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
 
 }  // namespace
 }  // namespace lin
+
+void linear_act_plan(int product, int64_t m, int64_t k, int64_t n, int64_t groups, int* tile, int* splits) {
+  lin::Plan p{};
+  if (product == 0) {
+    if (!groups && m <= lin::kSkinnyRows) {
+      *tile = -lin::skinny_waves(n);
+      *splits = 1;
+      return;
+    }
+    p = lin::ForwardLayout(m, k, n, groups).plan;
+  } else {
+    const lin::GradLayout at(m, k, n, groups);
+    p = product == 1 ? at.dx : at.dw;
+  }
+  *tile = p.tile;
+  *splits = p.splits;
+}
 
 size_t linear_act_workspace(int64_t m, int64_t k, int64_t n, int64_t groups) {
   return m > 0 ? lin::ForwardLayout(m, k, n, groups).total : 0;

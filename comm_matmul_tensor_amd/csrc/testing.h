@@ -26,6 +26,13 @@ extern "C" {
  * Always returns MC2_OK. */
 mc2_status mc2_testing_arrival(uint64_t wait_ticks, int raised_slabs);
 
+/* What mc2_linear_act (product 0) or mc2_linear_act_grad (1: dx, 2: dw) of
+ * these sizes runs: the tile of C, as numbered in linear_kernels.hpp, or minus
+ * the wavefronts of a workgroup where the product of few rows runs; and the
+ * parts of K.  Host code only. */
+mc2_status mc2_testing_linear_plan(int product, int64_t m, int64_t k, int64_t n, int64_t groups, int* tile,
+                                   int* splits);
+
 #ifdef __cplusplus
 }
 #endif
