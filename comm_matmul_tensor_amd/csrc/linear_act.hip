@@ -177,20 +177,27 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(Product p) {
 
 constexpr int64_t kSkinnyRows = 32;
 
-// Wavefronts of a workgroup: 4 where the columns make 1.5 to 4 workgroups per
-// CU, 16 where they make fewer (to cover HBM's latency) or more (fewer rows
-// of w read at a time).  One row, us with 4 / 16: 4096 x 7168 12.7 / 13.4,
-// 7168 x 4096 14.2 / 11.5, 8192 x 28672 92 / 84 (470 MB, 5.6 TB/s).
-int skinny_waves(int64_t n) {
+// Wavefronts of a workgroup: 16 while no CU has a second workgroup, to cover
+// HBM's latency (16 / 4, one row, in us: 4096 columns, k = 2048 6.3 / 7.6, 4096
+// 9.2 / 12.0, 16384 37.3 / 39.4; with k = 256, or 32 rows of k >= 4096, within 9 %
+// either way).  Past that 4, whose workgroups start and join sooner: 4112 columns,
+// k = 2048 7.7 / 7.8, 6144 18.3 / 16.7, 16384 51.1 / 41.4; 20480 columns, k = 256 6.8 /
+// 4.6, 1024 12.4 / 10.2; 32 rows of 8192 to 28672 columns, k = 4096, 5 to 6 % at any
+// width.  Only from a third workgroup per CU on do up to 16 rows of a long K
+// gain from 16 again (fewer rows of w read at a time): k = 2048, 8192 columns (two
+// per CU) 9.3 / 9.5, 9216 11.2 / 11.9; k = 6144, 8192 columns 22.1 / 22.8, 9216 28.3 /
+// 30.7; k = 8192, 28672 columns 86.6 / 92.8 (470 MB, 5.4 TB/s);
+// 16 rows, k = 2048 and 6144, 9216 columns 15.2 / 16.5 and 44.3 / 42.5.
+int skinny_waves(int64_t m, int64_t k, int64_t n) {
   const int64_t blocks = (n + 15) / 16;
-  return blocks >= 384 && blocks < 1024 ? 4 : 16;
+  return blocks <= 256 || (blocks > 512 && k >= 2048 && m <= 16) ? 16 : 4;
 }
 
 template <int DT, int MF>
 hipError_t launch_skinny(const Product& p, hipStream_t s) {
   const unsigned blocks = (unsigned)((p.n + 15) / 16);
   const bool vec = p.k % 8 == 0;
-  if (skinny_waves(p.n) == 4) {
+  if (skinny_waves(p.m, p.k, p.n) == 4) {
     if (vec) skinny_kernel<DT, MF, 4, true><<<blocks, 256, 0, s>>>(p);
     else skinny_kernel<DT, MF, 4, false><<<blocks, 256, 0, s>>>(p);
   } else {
@@ -453,7 +460,7 @@ void linear_act_plan(int product, int64_t m, int64_t k, int64_t n, int64_t group
   lin::Plan p{};
   if (product == 0) {
     if (!groups && m <= lin::kSkinnyRows) {
-      *tile = -lin::skinny_waves(n);
+      *tile = -lin::skinny_waves(m, k, n);
       *splits = 1;
       return;
     }

@@ -87,6 +87,14 @@ def test_every_arm_of_the_plan_is_named():
     assert len(found) > 40
 
 
+def test_few_rows_wavefronts():
+    """16 wavefronts up to one workgroup (16 columns) per CU, and for 16 rows at most of a long K from two on; else 4."""
+    for m, k, n, waves in [(1, 4096, 4096, 16), (1, 4096, 4097, 4), (32, 16384, 4096, 16), (32, 256, 4097, 4),
+                           (16, 2048, 8192, 4), (16, 2048, 8193, 16), (17, 2048, 8193, 4), (16, 2047, 8193, 4),
+                           (1, 1024, 28672, 4), (1, 8192, 28672, 16)]:
+        assert arm(FWD, m, k, n, 0)[2] == f"few rows, {waves}", (m, k, n)
+
+
 def test_plan_hook_refuses():
     t = ctypes.c_int()
     assert lib.mc2_testing_linear_plan(3, I(1), I(1), I(1), I(0), ctypes.byref(t), ctypes.byref(t)) == 4
