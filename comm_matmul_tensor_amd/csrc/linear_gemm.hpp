@@ -77,10 +77,6 @@ enum : int { DENSE = 0, BY_ROWS = 1, BY_K = 2 };
 
 struct RowRange { int64_t group, begin, end, tile, tiles; };
 
-// A value below 2^31 that every lane holds, as a scalar (buffer resources and
-// loop bounds made from it need no loop over lanes).
-__device__ __forceinline__ int64_t uniform(int64_t v) { return __builtin_amdgcn_readfirstlane((int)v); }
-
 // 64 groups from g0 on, one per lane: the rows [start, end) of the lane's
 // group, its tiles of bm rows, and the tiles of the 64 groups up to its own.
 // Range ends are read as ascending and at most m; `begin`, the end of the
