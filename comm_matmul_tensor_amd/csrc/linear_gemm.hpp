@@ -16,15 +16,19 @@
 //
 // Large products are bound by the MFMAs at the clock the card holds under them: 8192 x 8192 x 8192
 // 767 us, 1.43 PFLOP/s (as the vendor library's product on the same card);
-// 4096 x 7168 x 4096 with bias, gelu and z 204 us (1.18); its gradients' two
-// products 174 and 182 us (1.38, 1.32).  Measured and left out: loads ahead of
+// 4096 x 7168 x 4096 with bias, gelu and z 198 to 211 us on different cards (1.14 to
+// 1.21); its gradients' two products 174 and 182 us (1.38, 1.32).  In fp16, whose
+// 256 x 256 kernels keep 72 to 130 registers per lane in scratch around the
+// epilogue (bf16's none), 219 us where bf16 takes 198, and with the gradients'
+// dz pass 409 for 378.  Measured and left out: loads ahead of
 // time that only bring lines into the L2 (4 bytes per line, 1 to 6 steps
 // ahead; by every workgroup or by one per band) 5 to 40 % slower; K walked from
 // a step set by the tile, no change or 10 % slower; 256 x 224 tiles, which fill
 // the CUs better at n = 7168, within 5 % either way.  Products of one tile per
-// CU are bound by the LDS, which a step's loads and fragment reads pass: 517 x
-// 1792 x 4096 13.5 us (15.0 in 128 x 128 tiles), 256 x 4096 x 4096 14.8 (22.3),
-// 1024 x 1024 x 1024 8.7 (10.4).
+// CU are bound by the LDS, which a step's loads and fragment reads pass, and by
+// their first loads and epilogue, which nothing hides: 517 x 1792 x 4096 13.5 us
+// (15.0 in 128 x 128 tiles), 256 x 4096 x 4096 14.8 (22.3), 1024 x 1024 x 1024 8.7
+// (10.4).
 //
 // Groups of rows (experts): the tile's rows come from one group's range of
 // rows, found from the ranges on the device (find_tile), with that group's
@@ -442,8 +446,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     half(la1, la0, fb1, fb0, std::integral_constant<bool, true>(), cur, kt + NS, nxt, 0);
   };
   // The residual's values of this lane.  Where a wavefront has registers for
-  // them they are loaded before the main loop, which hides their latency
-  // (517 x 1792 x 4096 in fp16 by 128 x 128 tiles: 17.9 -> 17.4 us).
+  // them they are loaded before the main loop (517 x 1792 x 4096 in fp16 by 128 x
+  // 128 tiles: 17.4 us, 17.9 from the epilogue).  Their latency is not hidden:
+  // load4 tests the lane's place before each of them and its two forms write
+  // the same registers, so each waits for the one before, and the operands'
+  // first loads for all.  The same product by 96 x 128 tiles: 15.9 us, 13.7
+  // without the residual, 12.9 without the bias too, whose loads in the epilogue
+  // wait likewise; 4096 x 7168 x 4096: 168 us, 161 without the residual.
   const uint16_t* residual = static_cast<const uint16_t*>(p.residual);
   const bool quads = p.n % 4 == 0;
   const int64_t col0 = n0 + wn * WN + 4 * (lane / 16);  // this lane's first column

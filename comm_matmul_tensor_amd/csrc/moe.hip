@@ -14,7 +14,8 @@
 // the keys, expert then choice, below each of their own (permute_few).
 //
 // Rows.  All three row kernels go token by token, so that a token's row of x
-// or dout is read once for all its choices; HBM bound.
+// or dout is read once for all its choices; HBM bound (8192 tokens, 4 choices, h =
+// 4096: unpermute 52 us, 6.4 TB/s), but for the gradient of narrow rows.
 #include <algorithm>
 
 #include "layer_device.hpp"
@@ -344,7 +345,9 @@ __global__ __launch_bounds__(256) void unpermute_rows(UnpermuteArgs a, int tpr) 
 // its products with their rows of y are summed over the row.  TPR threads per
 // token (64: a wavefront, no barrier; 256: the workgroup), JB choices at a
 // time.  The last kZeroBlocks workgroups count the kept choices and clear the
-// rows of dy past them.
+// rows of dy past them.  Each counts the whole map, 128 loads a thread for 8192
+// tokens of 4 choices with few in flight: h = 64 takes 20 us, 256 23, where the
+// rows alone are 2 to 7; 512 40, 1024 49, 2048 58 (5.2 TB/s), 4096 124.
 template <int DT, bool VEC, int TPR, int JB>
 __global__ __launch_bounds__(256) void unpermute_grad(UnpermuteArgs a, int64_t token_blocks) {
   constexpr int WAVES = TPR / 64;

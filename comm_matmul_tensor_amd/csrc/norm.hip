@@ -273,7 +273,11 @@ hipError_t norm_dt(const NormArgs& a, hipStream_t st) {
 // A workgroup walks rows blockIdx.x, + gridDim.x, ...; thread t keeps the same
 // columns for every row, so dweight's sums stay in its registers until the
 // walk ends and go out as one row of fp32 partial sums per workgroup.
-// 8192 x 4096 with dsum: 52 us in all, 5.1 TB/s.
+// 8192 x 4096 with dsum: 52 us in all, 5.1 TB/s; 4096 x 8192 47.  Rows of more than
+// 8192 columns take 1024 threads of 128 registers, which do not hold the row, its
+// successor and the sums: 14 to 53 of them live in scratch with two chunks per
+// thread (4096 x 16384 167 us, 3.2 TB/s) and 198 to 744 with four (2048 x 32768 509
+// us, 1.1 TB/s).
 template <int DT, int TPR, int NCH, bool VEC>
 __global__ __launch_bounds__(TPR) void norm_grad_kernel(NormGradArgs a) {
   constexpr int WAVES = TPR / 64;
