@@ -8,17 +8,28 @@ namespace lin {
 namespace {
 
 // out = residual + act(sum of the parts + bias), z likewise; four columns per thread.
-template <int DT>
+// I8: the parts are int32 sums, added exactly and scaled.
+template <int DT, bool I8>
 __global__ __launch_bounds__(256) void join_kernel(Product p, int64_t ld, int64_t part) {
   const int64_t quads = (p.n + 3) / 4;
   const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (q >= quads * p.m) return;
   const int64_t row = q / quads, col = q % quads * 4;
   const float* src = p.partial + row * ld + col;
-  f32x4 v = *reinterpret_cast<const f32x4*>(src);
-#pragma unroll 4
-  for (int s = 1; s < p.splits; s++) v += *reinterpret_cast<const f32x4*>(src + s * part);
   const int n = p.n - col < 4 ? (int)(p.n - col) : 4;
+  f32x4 v;
+  if constexpr (I8) {
+    i32x4 c = *reinterpret_cast<const i32x4*>(src);
+#pragma unroll 4
+    for (int s = 1; s < p.splits; s++) c += *reinterpret_cast<const i32x4*>(src + s * part);
+    const f32x4 sb = load_scales(p.b_scale + col, n, p.n % 4 == 0);
+    const float sa = p.a_scale[row];
+    for (int r = 0; r < 4; r++) v[r] = ((float)c[r] * sa) * sb[r];
+  } else {
+    v = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll 4
+    for (int s = 1; s < p.splits; s++) v += *reinterpret_cast<const f32x4*>(src + s * part);
+  }
   const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
   const uint16_t* residual = static_cast<const uint16_t*>(p.residual);
   uint16_t* z = static_cast<uint16_t*>(p.z);
@@ -45,7 +56,7 @@ __global__ __launch_bounds__(256) void join_kernel(Product p, int64_t ld, int64_
   store(out, v);
 }
 
-template <int DT, int BM, int BN, int WGM, int WGN, int NS, bool AK, bool BK, int GMODE>
+template <int DT, int BM, int BN, int WGM, int WGN, int NS, bool AK, bool BK, int GMODE, bool I8>
 hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
   const int64_t tiles_m = (p.m + BM - 1) / BM + (GMODE == BY_ROWS ? p.groups : 0), tiles_n = (p.n + BN - 1) / BN;
   p.splits = plan.splits;
@@ -53,33 +64,40 @@ hipError_t launch_tile(Product p, const Plan& plan, hipStream_t s) {
   p.order_cols = GMODE != BY_ROWS && gemm::prefer_column_order(p.m, p.n, p.k, 2) ? 1 : 0;
   p.tile_group = gemm::choose_tile_group(tiles_m * BM, p.n, BM, BN, p.order_cols);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)(GMODE == BY_K ? p.groups : plan.splits));
-  product_kernel<DT, BM, BN, WGM, WGN, NS, AK, BK, GMODE><<<grid, 64 * WGM * WGN, 0, s>>>(p);
+  product_kernel<DT, BM, BN, WGM, WGN, NS, AK, BK, GMODE, I8><<<grid, 64 * WGM * WGN, 0, s>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || plan.splits < 2) return e;
   const int64_t ld = tiles_n * BN;
   const int64_t quads = (p.n + 3) / 4 * p.m;
-  join_kernel<DT><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, ld, tiles_m * BM * ld);
+  join_kernel<DT, I8><<<(unsigned)((quads + 255) / 256), 256, 0, s>>>(p, ld, tiles_m * BM * ld);
   return hipGetLastError();
 }
 
-template <int DT, bool AK, bool BK, int GMODE>
+template <int DT, bool AK, bool BK, int GMODE, bool I8 = false>
 hipError_t launch_layout(const Product& p, const Plan& plan, hipStream_t s) {
   if constexpr (AK) {
-    if (plan.tile == TILE_96X128) return launch_tile<DT, 96, 128, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
-    if (plan.tile == TILE_96X64) return launch_tile<DT, 96, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+    if (plan.tile == TILE_96X128) return launch_tile<DT, 96, 128, 2, 2, 4, AK, BK, GMODE, I8>(p, plan, s);
+    if (plan.tile == TILE_96X64) return launch_tile<DT, 96, 64, 2, 2, 4, AK, BK, GMODE, I8>(p, plan, s);
   }
   if constexpr (GMODE == DENSE)
-    if (plan.tile == TILE_128X64) return launch_tile<DT, 128, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+    if (plan.tile == TILE_128X64) return launch_tile<DT, 128, 64, 2, 2, 4, AK, BK, GMODE, I8>(p, plan, s);
   if constexpr (GMODE != BY_K)
-    if (plan.tile == TILE_64X64) return launch_tile<DT, 64, 64, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+    if (plan.tile == TILE_64X64) return launch_tile<DT, 64, 64, 2, 2, 4, AK, BK, GMODE, I8>(p, plan, s);
   switch (plan.tile) {
-    case TILE_256X256: return launch_tile<DT, 256, 256, 2, 4, 2, AK, BK, GMODE>(p, plan, s);
-    case TILE_128X256: return launch_tile<DT, 128, 256, 2, 4, 3, AK, BK, GMODE>(p, plan, s);
-    default: return launch_tile<DT, 128, 128, 2, 2, 4, AK, BK, GMODE>(p, plan, s);
+    case TILE_256X256: return launch_tile<DT, 256, 256, 2, 4, 2, AK, BK, GMODE, I8>(p, plan, s);
+    case TILE_128X256: return launch_tile<DT, 128, 256, 2, 4, 3, AK, BK, GMODE, I8>(p, plan, s);
+    default: return launch_tile<DT, 128, 128, 2, 2, 4, AK, BK, GMODE, I8>(p, plan, s);
   }
 }
 
 }  // namespace
+
+// Both operands K-contiguous codes.
+template <int DT>
+hipError_t launch_product_i8(const Product& p, int gmode, const Plan& plan, hipStream_t s) {
+  return gmode == BY_ROWS ? launch_layout<DT, true, true, BY_ROWS, true>(p, plan, s)
+                          : launch_layout<DT, true, true, DENSE, true>(p, plan, s);
+}
 
 template <int DT>
 hipError_t launch_product(const Product& p, int layout, int gmode, const Plan& plan, hipStream_t s) {

@@ -50,8 +50,13 @@ struct LinearGradArgs {
   int dtype, act;
   void *dx, *dw, *dbias;
   void* workspace;
+  // z and x as int8 codes with a scale per 128 columns (eight: x and z are NULL)
+  bool eight;
+  const int8_t *z_codes, *x_codes;
+  const float *z_scale, *x_scale;
+  int x_act;
 };
-size_t linear_act_grad_workspace(int64_t m, int64_t k, int64_t n, int64_t groups);
+size_t linear_act_grad_workspace(int64_t m, int64_t k, int64_t n, int64_t groups, bool eight = false);
 // The tile and the parts of K of a call's product (testing.h).
 void linear_act_plan(int product, int64_t m, int64_t k, int64_t n, int64_t groups, int* tile, int* splits);
 hipError_t launch_linear_act_grad(const LinearGradArgs& a, hipStream_t s);

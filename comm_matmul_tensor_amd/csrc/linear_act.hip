@@ -4,6 +4,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include "codes.hpp"
+#include "layer8_kernels.hpp"
 #include "linear_kernels.hpp"
 
 namespace mc2 {
@@ -228,8 +230,10 @@ struct DzArgs {
   const int32_t* offsets;
   int64_t groups;
   int tpr;
+  const int8_t* z_codes;  // EIGHT: z as codes, a scale per 128 columns
+  const float* z_scale;
 };
-template <int DT, int ACT, bool VEC>
+template <int DT, int ACT, bool VEC, bool EIGHT>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   __shared__ float red[256 * 8];  // [row of threads][column]
   int64_t m0 = (int64_t)blockIdx.x * kDzRows, m_end = a.m;
@@ -250,7 +254,10 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
       unpack8<DT>(load_chunk<VEC>(a.dout + row * a.n, c, a.n), d);
       if constexpr (ACT != ACT_NONE) {
         float f[8];
-        unpack8<DT>(load_chunk<VEC>(a.z + row * a.n, c, a.n), f);
+        if constexpr (EIGHT)
+          code_values(load_codes<VEC>(a.z_codes + row * a.n, c, a.n), a.z_scale[row * scales_of(a.n, 128) + c / 128], f);
+        else
+          unpack8<DT>(load_chunk<VEC>(a.z + row * a.n, c, a.n), f);
 #pragma unroll
         for (int e = 0; e < 8; e++) d[e] *= act_slope<ACT>(f[e]);
       }
@@ -309,8 +316,13 @@ hipError_t launch_dz(DzArgs a, int act, void* dbias, hipStream_t s) {
     const dim3 grid((unsigned)tiles, (unsigned)((a.n + 8 * a.tpr - 1) / (8 * a.tpr)));
     with_act(act, [&](auto ACT_) {
       constexpr int ACT = decltype(ACT_)::value;
-      if (vec) dz_kernel<DT, ACT, true><<<grid, 256, 0, s>>>(a);
-      else dz_kernel<DT, ACT, false><<<grid, 256, 0, s>>>(a);
+      if (a.z_codes && ACT != ACT_NONE) {
+        if (vec) dz_kernel<DT, ACT, true, true><<<grid, 256, 0, s>>>(a);
+        else dz_kernel<DT, ACT, false, true><<<grid, 256, 0, s>>>(a);
+      } else {
+        if (vec) dz_kernel<DT, ACT, true, false><<<grid, 256, 0, s>>>(a);
+        else dz_kernel<DT, ACT, false, false><<<grid, 256, 0, s>>>(a);
+      }
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -351,13 +363,13 @@ struct ForwardLayout {
 struct GradLayout {
   size_t dz, sums, x8, w8, partial, total;
   Plan dx, dw;
-  GradLayout(int64_t m, int64_t k, int64_t n, int64_t groups) {
+  GradLayout(int64_t m, int64_t k, int64_t n, int64_t groups, bool eight = false) {
     Parts p;
     dx = plan_product(m, k, n, 1, groups ? BY_ROWS : DENSE, groups);
     dw = plan_product(n, k, m, 2, groups ? BY_K : DENSE, groups);
     dz = p.take((size_t)m * pad8(n) * 2);
     sums = p.take((size_t)dz_tiles(m, groups) * n * sizeof(float));
-    x8 = p.take(k % 8 ? (size_t)m * pad8(k) * 2 : 0);
+    x8 = p.take(k % 8 || eight ? (size_t)m * pad8(k) * 2 : 0);  // x padded, or widened from its codes
     w8 = p.take(k % 8 ? (size_t)std::max<int64_t>(groups, 1) * n * pad8(k) * 2 : 0);
     partial = p.take(std::max(dx.partial_bytes, dw.partial_bytes));
     total = p.used;
@@ -399,7 +411,7 @@ hipError_t forward_dt(const LinearArgs& a, hipStream_t s) {
 
 template <int DT>
 hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
-  const GradLayout at(a.m, a.k, a.n, a.groups);
+  const GradLayout at(a.m, a.k, a.n, a.groups, a.eight);
   char* ws = static_cast<char*>(a.workspace);
   const int64_t matrices = std::max<int64_t>(a.groups, 1);
   // dz: dout itself without an activation, where its rows are aligned
@@ -407,6 +419,8 @@ hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
   DzArgs d{};
   d.dout = static_cast<const uint16_t*>(a.dout);
   d.z = static_cast<const uint16_t*>(a.z);
+  d.z_codes = a.z_codes;
+  d.z_scale = a.z_scale;
   d.dz = products && copy ? reinterpret_cast<uint16_t*>(ws + at.dz) : nullptr;
   d.partial = a.dbias ? reinterpret_cast<float*>(ws + at.sums) : nullptr;
   d.m = a.m;
@@ -419,10 +433,26 @@ hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
   const void *x = a.x, *w = a.w, *dz = copy ? d.dz : a.dout;
   if (a.k % 8) {
     // x for dw, w for dx
-    e = launch_pad_rows(a.x, a.dw ? a.m : 0, ws + at.x8, a.w, a.dx ? matrices * a.n : 0, ws + at.w8, a.k, s);
+    e = launch_pad_rows(a.x, a.dw && !a.eight ? a.m : 0, ws + at.x8, a.w, a.dx ? matrices * a.n : 0, ws + at.w8, a.k, s);
     if (e != hipSuccess) return e;
     x = ws + at.x8;
     w = ws + at.w8;
+  }
+  if (a.eight && a.dw && a.m > 0) {
+    // x's values in 16 bits, which the product reads in many tiles: 4096 x 4096 in 13 us of 390
+    CodeArgs c{};
+    c.codes_in = a.x_codes;
+    c.scale_in = a.x_scale;
+    c.out = ws + at.x8;
+    c.rows = a.m;
+    c.cols = a.k;
+    c.ld = pad8(a.k);
+    c.group = 128;
+    c.dtype = a.dtype;
+    c.act = a.x_act;
+    e = launch_dequant_rows(c, s);
+    if (e != hipSuccess) return e;
+    x = ws + at.x8;
   }
   Product p{};
   p.offsets = a.offsets;
@@ -480,8 +510,8 @@ void linear_act_plan(int product, int64_t m, int64_t k, int64_t n, int64_t group
 size_t linear_act_workspace(int64_t m, int64_t k, int64_t n, int64_t groups) {
   return m > 0 ? lin::ForwardLayout(m, k, n, groups).total : 0;
 }
-size_t linear_act_grad_workspace(int64_t m, int64_t k, int64_t n, int64_t groups) {
-  return lin::GradLayout(m, k, n, groups).total;
+size_t linear_act_grad_workspace(int64_t m, int64_t k, int64_t n, int64_t groups, bool eight) {
+  return lin::GradLayout(m, k, n, groups, eight).total;
 }
 
 hipError_t launch_linear_act(const LinearArgs& a, hipStream_t s) {

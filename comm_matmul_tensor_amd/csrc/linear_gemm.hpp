@@ -3,6 +3,12 @@
 //   C (m, n) = A (m, k) @ B (k, n), 16-bit operands, fp32 accumulation, then
 //   z = C + bias, out = residual + act(z), rounded once.
 //
+// The same loop runs the int8 product of mc2_linear_i8 (I8): a row of K codes
+// is a row of K / 2 pairs, moved, stored and read as 16-bit elements are; only
+// the MFMA differs (16 x 16 x 64 codes for 16 x 16 x 32 elements, in as many
+// cycles), and the epilogue first turns the int32 sums into
+// z = (C x_scale) w_scale + bias.  Below, K and leading dimensions count pairs.
+//
 // Operands: A K-contiguous (AK: stored (m, k)) or M-contiguous ((k, m)); B
 // K-contiguous (BK: (n, k)) or N-contiguous ((k, n)).  Their leading
 // dimensions are multiples of 8 elements (the launcher copies others), so
@@ -75,6 +81,7 @@ struct Product {
   int64_t k_part;
   float* partial;
   int tile_group, order_cols;       // order of the tiles (tile_at)
+  const float *a_scale, *b_scale;   // I8: of A's rows, of C's columns (group g's at g n)
 };
 
 enum : int { DENSE = 0, BY_ROWS = 1, BY_K = 2 };
@@ -226,6 +233,17 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// The int8 product accumulates int32 in the same registers.
+template <int DT, bool I8>
+__device__ __forceinline__ f32x4 mfma_any(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (I8)
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                                           __builtin_bit_cast(i32x4, b),
+                                                                           __builtin_bit_cast(i32x4, c), 0, 0, 0));
+  else
+    return mfma16<DT>(a, b, c);
+}
+
 // Workgroup `block`'s place among the tiles: blocks are dealt to the 8 XCDs in
 // turn, so each XCD gets a contiguous eighth of them.
 __device__ __forceinline__ int tile_place(int block, int tiles) {
@@ -300,6 +318,17 @@ __device__ __forceinline__ u32x2 load4(const uint16_t* p, int64_t left, bool qua
   }
   return v;
 }
+__device__ __forceinline__ f32x4 load_scales(const float* p, int64_t left, bool quads) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (quads) {
+    if (left > 0) v = *reinterpret_cast<const f32x4*>(p);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+      if (r < left) v[r] = p[r];
+  }
+  return v;
+}
 template <int DT>
 __device__ __forceinline__ f32x4 widen4(u32x2 v) {
   return f32x4{dec16<DT>(v[0]), dec16<DT>(v[0] >> 16), dec16<DT>(v[1]), dec16<DT>(v[1] >> 16)};
@@ -308,7 +337,7 @@ __device__ __forceinline__ f32x4 widen4(u32x2 v) {
 // Element r of accumulator (i, j) of lane l is C at row 16 i + l % 16 and
 // column 16 j + 4 (l / 16) + r of the wavefront's block (the MFMAs take B's
 // fragment first, so they make C transposed).
-template <int DT, int BM, int BN, int WGM, int WGN, int NS, bool AK, bool BK, int GMODE>
+template <int DT, int BM, int BN, int WGM, int WGN, int NS, bool AK, bool BK, int GMODE, bool I8 = false>
 __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host needs only the symbol to launch)
   constexpr int NT = 64 * WGM * WGN;
@@ -327,6 +356,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
   const uint16_t* a = static_cast<const uint16_t*>(p.a);
   const uint16_t* b = static_cast<const uint16_t*>(p.b);
   const uint16_t* bias = static_cast<const uint16_t*>(p.bias);
+  const float* b_scale = p.b_scale;
+  bool scaled = I8;
   if constexpr (GMODE == BY_ROWS) {
     // The grid has room for a partial tile in every group; the tiles there are
     // go group by group, in bands of rows within each, spread over all XCDs.
@@ -341,9 +372,11 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     if (r.group == p.groups) {  // rows of no group: z = 0
       k_len = 0;
       bias = nullptr;
+      scaled = false;  // (their scales may be anything)
     } else {
       b += r.group * p.b_group;
       if (bias) bias += r.group * p.n;
+      if constexpr (I8) b_scale += r.group * p.n;
     }
   } else {
     tile_at(tile_place((int)blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, p.order_cols, p.tile_group, tm, tn);
@@ -414,7 +447,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
 #pragma unroll
       for (int j = 0; j < FN; j++) {
         const int q = i * FN + j;
-        acc[i][j] = mfma16<DT>(fb[j], i < FM - 1 ? fa[i < FM - 1 ? i : 0] : last, acc[i][j]);
+        acc[i][j] = mfma_any<DT, I8>(fb[j], i < FM - 1 ? fa[i < FM - 1 ? i : 0] : last, acc[i][j]);
         if (i > 0 && j == 0) fa[i - 1] = ra.read_one(from, kk, i - 1);
         if (i == 0 && j == FN - 1) next_last = ra.read_one(from, kk, FM - 1);
         if (const int f = read_of_b(q); f < FN) nb[f] = rb.read_one(from + kATile, kk, f);
@@ -530,6 +563,23 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     const int row = wm * WM + 16 * i + lane % 16, col = wn * WN + 16 * j + 4 * (lane / 16);
     return reinterpret_cast<u32x2*>((row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col);
   };
+  if constexpr (I8) {
+    // (zeros where nothing is stored, and for rows of no group: their sums are 0)
+    f32x4 sb[FN];
+#pragma unroll
+    for (int j = 0; j < FN; j++) sb[j] = load_scales(b_scale + col0 + 16 * j, scaled ? p.n - col0 - 16 * j : 0, quads);
+#pragma unroll
+    for (int i = 0; i < FM; i++) {
+      const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
+      const float sa = scaled && row < m_end ? p.a_scale[row] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < FN; j++) {
+        const i32x4 c = __builtin_bit_cast(i32x4, acc[i][j]);
+#pragma unroll
+        for (int r = 0; r < 4; r++) acc[i][j][r] = ((float)c[r] * sa) * sb[j][r];
+      }
+    }
+  }
   if (bias) {
 #pragma unroll
     for (int j = 0; j < FN; j++) {

@@ -1,5 +1,5 @@
 // Launches shared by the linear's translation units: the tiled product
-// (gemm_linear_bf16.hip, gemm_linear_f16.hip) and the plan it follows.
+// (gemm_linear_bf16.hip, gemm_linear_f16.hip, gemm_linear_i8.hip) and the plan it follows.
 #pragma once
 #include "linear_gemm.hpp"
 
@@ -29,6 +29,9 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
 // and epilogue are set here from the plan.
 template <int DT>
 hipError_t launch_product(const Product& p, int layout, int gmode, const Plan& plan, hipStream_t s);
+// The same of int8 codes (layout 0; sizes in pairs of codes, scales set), rounded to DT (gemm_linear_i8.hip).
+template <int DT>
+hipError_t launch_product_i8(const Product& p, int gmode, const Plan& plan, hipStream_t s);
 
 }  // namespace lin
 }  // namespace mc2

@@ -1,0 +1,218 @@
+// K14: rows to int8 codes with a scale per row or per 128 columns, and back.
+//
+//   a = max |x|, scale = a / 127, code = rint(x / scale); out = act(code scale)
+//
+// Bound by HBM: a row is read once, kept in registers across its maximum and
+// its codes written once.  The division is the IEEE one, so that the codes are
+// those of the formula.
+//
+// Per 128 columns the 16 lanes that hold a group's chunks of 8 find its
+// maximum by DPP; nothing else depends on the row, so threads take chunks of
+// rows in any shape: `tpr` of them a row.  Per row a team of TPR threads holds
+// it with NCH chunks each; rows that do not fit are read twice (quant_wide).
+#include <algorithm>
+
+#include "codes.hpp"
+#include "layer8_kernels.hpp"
+#include "linear_act.hpp"
+
+namespace mc2 {
+namespace {
+
+__device__ __forceinline__ float scale_of(uint32_t top_bits) { return __uint_as_float(top_bits) / 127.0f; }
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; e++) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);  // (a NaN is the largest)
+  return m;
+}
+// A scale that is 0, NaN or infinite gives codes 0.
+__device__ __forceinline__ u32x2 codes_of(const float (&x)[8], float scale) {
+  u32x2 r = {0u, 0u};
+  if (!(scale > 0.0f && scale < __builtin_inff())) return r;
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    const float q = fminf(fmaxf(x[e] / scale, -127.0f), 127.0f);
+    r[e / 4] |= ((uint32_t)(int)__builtin_rintf(q) & 0xFFu) << (8 * (e & 3));
+  }
+  return r;
+}
+template <bool VEC>
+__device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t cols, u32x2 v) {
+  if (VEC || c + 8 <= cols) {
+    __builtin_memcpy(row + c, &v, 8);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (c + e < cols) row[c + e] = (int8_t)(v[e / 4] >> (8 * (e & 3)));
+  }
+}
+
+// Threads of a row for `chunks` chunks: the power of two from `least` to 256
+// that leaves the fewest idle in a row's last turn, the larger of two alike.
+int row_threads(int64_t chunks, int least) {
+  int best = least;
+  int64_t waste = INT64_MAX;
+  for (int t = least; t <= 256; t *= 2) {
+    const int64_t w = (chunks + t - 1) / t * t - chunks;
+    if (w <= waste) {
+      waste = w;
+      best = t;
+    }
+    if (t >= chunks) break;
+  }
+  return best;
+}
+
+// ---------------------------------------------------------------- per 128 columns
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void quant_groups(CodeArgs a, int tpr) {
+  const int64_t row = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
+  if (row >= a.rows) return;  // (whole teams of 16 lanes: tpr is a multiple of 16)
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.cols;
+  int8_t* codes = a.codes + row * a.cols;
+  float* scales = a.scale + row * scales_of(a.cols, 128);
+  const int64_t last = (a.cols + 127) / 128 * 128;  // a group's lanes all take part
+#pragma unroll 4
+  for (int64_t c = 8 * (int64_t)(threadIdx.x % tpr); c < last; c += 8 * tpr) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (c < a.cols) v = load_chunk<VEC>(x, c, a.cols);
+    float f[8];
+    unpack8<DT>(v, f);
+    const float scale = scale_of(max16(top_of(f)));
+    if (c >= a.cols) continue;
+    if (c % 128 == 0) scales[c / 128] = scale;
+    store_codes<VEC>(codes, c, a.cols, codes_of(f, scale));
+  }
+}
+
+// ---------------------------------------------------------------- per row
+template <int DT, int TPR, int NCH, bool VEC>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quant_row(CodeArgs a) {
+  constexpr int WAVES = TPR / 64;
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  __shared__ uint32_t red[WAVES];
+  const int t = RPB > 1 ? threadIdx.x % TPR : threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
+  if (RPB > 1 && row >= a.rows) return;  // RPB > 1: no barrier below
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.cols;
+  u32x4 v[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; i++) {
+    const int64_t c = 8 * (int64_t)(t + i * TPR);
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (c < a.cols) v[i] = load_chunk<VEC>(x, c, a.cols);
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NCH; i++) {
+    float f[8];
+    unpack8<DT>(v[i], f);
+    top = max(top, top_of(f));
+  }
+  const float scale = scale_of(block_max<WAVES>(top, red));
+  if (t == 0) a.scale[row] = scale;
+#pragma unroll
+  for (int i = 0; i < NCH; i++) {
+    const int64_t c = 8 * (int64_t)(t + i * TPR);
+    float f[8];
+    unpack8<DT>(v[i], f);
+    if (c < a.cols) store_codes<VEC>(a.codes + row * a.cols, c, a.cols, codes_of(f, scale));
+  }
+}
+
+constexpr int kWide = 1024;
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kWide) void quant_wide(CodeArgs a) {
+  __shared__ uint32_t red[kWide / 64];
+  const int64_t row = blockIdx.x;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + row * a.cols;
+  uint32_t top = 0;
+  for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.cols; c += 8 * kWide) {
+    float f[8];
+    unpack8<DT>(load_chunk<VEC>(x, c, a.cols), f);
+    top = max(top, top_of(f));
+  }
+  const float scale = scale_of(block_max<kWide / 64>(top, red));
+  if (threadIdx.x == 0) a.scale[row] = scale;
+  for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.cols; c += 8 * kWide) {
+    float f[8];
+    unpack8<DT>(load_chunk<VEC>(x, c, a.cols), f);
+    store_codes<VEC>(a.codes + row * a.cols, c, a.cols, codes_of(f, scale));
+  }
+}
+
+template <int DT, bool VEC>
+hipError_t quant_launch(const CodeArgs& a, hipStream_t s) {
+  if (a.group) {
+    const int tpr = row_threads((a.cols + 127) / 128 * 16, 16), per = 256 / tpr;
+    quant_groups<DT, VEC><<<(unsigned)((a.rows + per - 1) / per), 256, 0, s>>>(a, tpr);
+    return hipGetLastError();
+  }
+  auto wave = [&](auto NCH_) {
+    quant_row<DT, 64, decltype(NCH_)::value, VEC><<<(unsigned)((a.rows + 3) / 4), 256, 0, s>>>(a);
+  };
+  using std::integral_constant;
+  const int64_t h = a.cols;
+  if (h <= 512) wave(integral_constant<int, 1>());
+  else if (h <= 1024) wave(integral_constant<int, 2>());
+  else if (h <= 2048) quant_row<DT, 256, 1, VEC><<<(unsigned)a.rows, 256, 0, s>>>(a);
+  else if (h <= 4096) quant_row<DT, 512, 1, VEC><<<(unsigned)a.rows, 512, 0, s>>>(a);
+  else if (h <= 8192) quant_row<DT, 512, 2, VEC><<<(unsigned)a.rows, 512, 0, s>>>(a);
+  else if (h <= 16384) quant_row<DT, 1024, 2, VEC><<<(unsigned)a.rows, 1024, 0, s>>>(a);
+  else if (h <= 32768) quant_row<DT, 1024, 4, VEC><<<(unsigned)a.rows, 1024, 0, s>>>(a);
+  else quant_wide<DT, VEC><<<(unsigned)a.rows, kWide, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- and back
+// out's rows are ld apart (a multiple of 8 and the columns past the last one
+// become 0, or cols).
+template <int DT, int ACT, bool VEC>
+__global__ __launch_bounds__(256) void dequant_kernel(CodeArgs a, int tpr) {
+  const int64_t row = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
+  if (row >= a.rows) return;
+  const int8_t* codes = a.codes_in + row * a.cols;
+  const float* scales = a.scale_in + row * scales_of(a.cols, a.group);
+  uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ld;
+#pragma unroll 4
+  for (int64_t c = 8 * (int64_t)(threadIdx.x % tpr); c < a.ld; c += 8 * tpr) {
+    float f[8];
+    code_values(load_codes<VEC>(codes, c, a.cols), scales[scale_at(c < a.cols ? c : 0, a.group)], f);
+#pragma unroll
+    for (int e = 0; e < 8; e++) f[e] = VEC || c + e < a.cols ? act_of<ACT>(f[e]) : 0.0f;
+    store_chunk<VEC, true>(out, c, a.ld, pack8<DT>(f));
+  }
+}
+
+template <int DT, int ACT>
+hipError_t dequant_launch(const CodeArgs& a, hipStream_t s) {
+  const int tpr = row_threads((a.cols + 7) / 8, 1), per = 256 / tpr;
+  const unsigned blocks = (unsigned)((a.rows + per - 1) / per);
+  if (a.cols % 8 == 0) dequant_kernel<DT, ACT, true><<<blocks, 256, 0, s>>>(a, tpr);
+  else dequant_kernel<DT, ACT, false><<<blocks, 256, 0, s>>>(a, tpr);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant_rows(const CodeArgs& a, hipStream_t s) {
+  if (a.rows < 1 || a.cols < 1 || (a.group != 0 && a.group != 128)) return hipErrorInvalidValue;
+  const bool vec = a.cols % 8 == 0;
+  if (a.dtype == DT_BF16) return vec ? quant_launch<DT_BF16, true>(a, s) : quant_launch<DT_BF16, false>(a, s);
+  return vec ? quant_launch<DT_F16, true>(a, s) : quant_launch<DT_F16, false>(a, s);
+}
+
+hipError_t launch_dequant_rows(const CodeArgs& given, hipStream_t s) {
+  CodeArgs a = given;
+  if (a.ld == 0) a.ld = a.cols;
+  if (a.rows < 1 || a.cols < 1 || a.ld < a.cols || (a.group != 0 && a.group != 128)) return hipErrorInvalidValue;
+  hipError_t e = hipErrorInvalidValue;
+  with_act(a.act, [&](auto ACT_) {
+    constexpr int ACT = decltype(ACT_)::value;
+    e = a.dtype == DT_BF16 ? dequant_launch<DT_BF16, ACT>(a, s) : dequant_launch<DT_F16, ACT>(a, s);
+  });
+  return e;
+}
+
+}  // namespace mc2

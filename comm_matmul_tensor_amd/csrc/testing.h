@@ -32,6 +32,8 @@ mc2_status mc2_testing_arrival(uint64_t wait_ticks, int raised_slabs);
  * parts of K.  Host code only. */
 mc2_status mc2_testing_linear_plan(int product, int64_t m, int64_t k, int64_t n, int64_t groups, int* tile,
                                    int* splits);
+/* The same of mc2_linear_i8. */
+mc2_status mc2_testing_linear_i8_plan(int64_t m, int64_t k, int64_t n, int64_t groups, int* tile, int* splits);
 
 #ifdef __cplusplus
 }

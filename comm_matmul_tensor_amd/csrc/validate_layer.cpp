@@ -3,50 +3,10 @@
 #include "validate_layer.hpp"
 
 #include <cmath>
-#include <initializer_list>
+
+#include "validate_util.hpp"
 
 namespace mc2 {
-
-namespace {
-
-using std::string;
-
-constexpr int64_t kRows = (int64_t)1 << 24, kWidth = (int64_t)1 << 24, kDim = (int64_t)1 << 21,
-                  kTokens = (int64_t)1 << 23, kGroups = 4096, kGroupWidth = (int64_t)1 << 29;
-
-bool is_half(mc2_dtype d) { return d == MC2_F16 || d == MC2_BF16; }
-string str(int64_t v) { return std::to_string(static_cast<long long>(v)); }
-
-mc2_status shape(const char* who, const string& what) { return fail(MC2_ERR_SHAPE, string(who) + ": " + what); }
-
-// Every pointer 16-byte aligned (NULL is).
-mc2_status aligned(const char* who, std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (reinterpret_cast<uintptr_t>(p) & 15u)
-      return fail(MC2_ERR_ALIGN, string(who) + ": tensor not 16-byte aligned");
-  return MC2_OK;
-}
-mc2_status required(const char* who, std::initializer_list<const void*> ps, const char* names) {
-  for (const void* p : ps)
-    if (!p) return fail(MC2_ERR_NULL, string(who) + ": " + names + " are required");
-  return MC2_OK;
-}
-mc2_status half(const char* who, mc2_dtype d) {
-  return is_half(d) ? MC2_OK : fail(MC2_ERR_DTYPE, string(who) + ": dtype must be F16 or BF16");
-}
-mc2_status workspace_ok(const char* who, const void* ws, size_t bytes, size_t needed) {
-  if (needed > 0 && (!ws || bytes < needed))
-    return fail(MC2_ERR_WORKSPACE, string(who) + ": workspace needs " + std::to_string(needed) + " bytes");
-  return needed > 0 ? aligned(who, {ws}) : MC2_OK;
-}
-
-#define MC2_TRY(call)                \
-  do {                               \
-    mc2_status s_ = (call);          \
-    if (s_ != MC2_OK) return s_;     \
-  } while (0)
-
-}  // namespace
 
 mc2_status check_norm_sizes(const char* who, int64_t rows, int64_t h) {
   if (rows < 0 || rows >= kRows) return shape(who, "rows must lie in [0, 2^24), got " + str(rows));
@@ -95,7 +55,6 @@ mc2_status check_linear_sizes(const char* who, int64_t m, int64_t k, int64_t n, 
   return MC2_OK;
 }
 
-namespace {
 mc2_status check_linear_kind(const char* who, const void* group_offsets, int64_t groups, mc2_dtype dtype,
                              mc2_act act) {
   MC2_TRY(half(who, dtype));
@@ -105,7 +64,6 @@ mc2_status check_linear_kind(const char* who, const void* group_offsets, int64_t
   if (groups == 0 && group_offsets) return shape(who, "group_offsets without groups");
   return MC2_OK;
 }
-}  // namespace
 
 mc2_status check_linear_act(const void* x, const void* w, const void* bias, const void* residual, int64_t m, int64_t k,
                             int64_t n, const void* group_offsets, int64_t groups, mc2_dtype dtype, mc2_act act,

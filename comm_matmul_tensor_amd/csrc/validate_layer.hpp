@@ -13,6 +13,8 @@ mc2_status check_add_rms_norm_grad(const void* dout, const void* dsum, const voi
                                    const void* rstd, int64_t rows, int64_t h, mc2_dtype dtype, const void* dx,
                                    const void* dweight, const void* workspace, size_t workspace_bytes, size_t needed);
 mc2_status check_linear_sizes(const char* who, int64_t m, int64_t k, int64_t n, int64_t groups);
+mc2_status check_linear_kind(const char* who, const void* group_offsets, int64_t groups, mc2_dtype dtype,
+                             mc2_act act);
 mc2_status check_linear_act(const void* x, const void* w, const void* bias, const void* residual, int64_t m, int64_t k,
                             int64_t n, const void* group_offsets, int64_t groups, mc2_dtype dtype, mc2_act act,
                             const void* out, const void* z_out, const void* workspace, size_t workspace_bytes,

@@ -241,9 +241,10 @@ def mc2_add_rms_norm_grad(dout: torch.Tensor, s: torch.Tensor, weight: torch.Ten
 
 
 # ------------------------------------------------------------------ linear
-def _linear_sizes(x, w, group_offsets):
+def _linear_sizes(x, w, group_offsets, half: bool = True, w_dtype: Optional[torch.dtype] = None):
     m, k = _tensor(x, "x", 2)
-    _half(x, "x")
+    if half:
+        _half(x, "x")
     groups = 0
     if group_offsets is not None:
         (size,) = _tensor(group_offsets, "group_offsets", 1)
@@ -253,7 +254,7 @@ def _linear_sizes(x, w, group_offsets):
         if group_offsets.dtype != _I32:
             raise TypeError(f"group_offsets has dtype {group_offsets.dtype}, expected torch.int32")
     n = _tensor(w, "w", 3 if groups else 2)[-2]
-    _needed(w, "w", (groups, n, k) if groups else (n, k), x.dtype)
+    _needed(w, "w", (groups, n, k) if groups else (n, k), w_dtype or x.dtype)
     return m, k, n, groups
 
 
