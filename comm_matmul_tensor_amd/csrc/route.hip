@@ -3,16 +3,24 @@
 //   p = softmax(l) or sigmoid(l), c = p + bias; the top largest c of the kept
 //   groups; weights = scale p (/ the sum of the chosen p)
 //
-// One wavefront takes a token: lane i holds the logits i, i + 64, ... in SLOTS
-// registers, so that a row is read once in whole lines and every reduction is
-// one of DPP steps.  The choice goes by rounds: the wavefront's largest key,
-// then the lowest register and lane that hold it.
+// A team of TEAM lanes takes a token: lane i of it holds the logits i, i +
+// TEAM, ... in SLOTS registers.  The choice goes by rounds (pick): the team's
+// largest key, the lowest expert that has it, on to those below.  Teams of 16
+// lanes (up to 256 experts and 16 choices) reduce by DPP alone, four tokens at a
+// time; larger ones take a wavefront.  Bound by these instructions and their
+// latency, not by memory (8.4 MB at the copy's rate would take 2 us): 8191
+// tokens x 256 fp32 logits, top 8: 6.6 us in a graph of such calls, where an
+// empty kernel takes 3; with bias 8.9, with 16 groups of which 6 are kept too
+// 12.  (A wavefront a token, its rounds by ballots: 8.6 and 19; loads each
+// under a condition, which are waited for one by one: 11 and 22.)
 //
 // Order.  Without a bias the keys are the logits themselves: p rises with l,
 // so no score is formed but those of the chosen.  Otherwise c is formed in
-// fp32 with an error bound (below), and a row in which two neighbours of the
-// order lie within it, a tie among them, is done again in fp64 (choose64): the
-// experts chosen are those of fp64, at fp32's cost.
+// fp32 with an error bound (Doubt).  Where two neighbours of the order lie
+// within it, a tie among them, fp64 decides: on the chosen and the next few
+// alone where that is enough (order64), else on the whole row (choose64), 3
+// us for the rows of a batch that need it.  So the experts chosen are those of
+// fp64, at fp32's cost.
 #include "layer8_kernels.hpp"
 #include "layer_device.hpp"
 
@@ -22,7 +30,7 @@ namespace {
 constexpr float kLog2eHi = 1.44269504088896340736f;
 constexpr float kLog2eLo = 1.925963033500e-8f;  // log2(e) - kLog2eHi
 constexpr float kLn2 = 0.693147180559945309417f;
-constexpr int kOff = INT32_MIN;                 // key of an expert that is off
+constexpr uint32_t kOff = 0;                    // key of an expert that is off; all others are larger
 
 // exp(x) within 2^-22: the argument in base 2 to twice fp32's precision (x log2(e)
 // rounded alone is off by |x| 2^-24).  Past +-200 it is 0 or infinite in fp32.
@@ -45,22 +53,59 @@ __device__ __forceinline__ void store_logit(void* p, int64_t i, float f) {
   else static_cast<uint16_t*>(p)[i] = enc16<DT>(f);
 }
 
-// Floats in an order of signed integers (no NaN; -0 has been added to 0).
-__device__ __forceinline__ int key_of(float f) {
-  const int b = __float_as_int(f);
-  return b ^ ((b >> 31) & 0x7FFFFFFF);
+// Floats in an order of unsigned integers (no NaN; -0 has been added to 0).
+__device__ __forceinline__ uint32_t key_of(float f) {
+  const uint32_t b = __float_as_uint(f);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float of_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
-// Maximum over the wavefront, as a scalar.
-__device__ __forceinline__ int wave_max_key(int v) {
-  v = max(v, (int)dpp16<0>((uint32_t)v));
-  v = max(v, (int)dpp16<1>((uint32_t)v));
-  v = max(v, (int)dpp16<2>((uint32_t)v));
-  v = max(v, (int)dpp16<3>((uint32_t)v));
-  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x142, 0xA, 0xF, false));  // row_bcast 15
-  v = max(v, __builtin_amdgcn_update_dpp(v, v, 0x143, 0xC, 0xF, false));  // row_bcast 31
-  return __builtin_amdgcn_readlane(v, 63);
+// Maximum over the team, in all of its lanes.
+template <int TEAM>
+__device__ __forceinline__ uint32_t team_max(uint32_t v) {
+  v = max16(v);
+  if constexpr (TEAM == 64) {
+    const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16),
+                   c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
+    v = max(max(a, b), max(c, d));
+  }
+  return v;
+}
+// The team's first lane that says `is` (some lane does).
+template <int TEAM>
+__device__ __forceinline__ int first_lane(bool is) {
+  const unsigned long long at = __ballot(is);
+  if constexpr (TEAM == 64) return __ffsll((long long)at) - 1;
+  const int wlane = threadIdx.x % 64;
+  const uint32_t half = wlane & 32 ? (uint32_t)(at >> 32) : (uint32_t)at;
+  return __ffs((int)(half >> (wlane & 16) & 0xFFFFu)) - 1;
+}
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v) {
+  if constexpr (TEAM == 64) return wave_sum(v);
+  v += __uint_as_float(dpp16<0>(__float_as_uint(v)));
+  v += __uint_as_float(dpp16<1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp16<2>(__float_as_uint(v)));
+  return v + __uint_as_float(dpp16<3>(__float_as_uint(v)));
+}
+// f over the wavefront's doubles, as a scalar.
+template <int STEP>
+__device__ __forceinline__ double dpp16d(double v) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{dpp16<STEP>(b[0]), dpp16<STEP>(b[1])});
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const u32x2 b = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)b[0], lane),
+                                          (uint32_t)__builtin_amdgcn_readlane((int)b[1], lane)});
+}
+template <typename F>
+__device__ __forceinline__ double wave_fold(double v, F f) {
+  v = f(v, dpp16d<0>(v));
+  v = f(v, dpp16d<1>(v));
+  v = f(v, dpp16d<2>(v));
+  v = f(v, dpp16d<3>(v));
+  return f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
 }
 
 // What rounding can move between two values that are compared.  p of a
@@ -75,41 +120,71 @@ struct Doubt {
   }
 };
 
-// The top largest keys: lane j < top gets the j-th's expert (-1: none left).
-// CHECK: false where the order of two of them, or of the last and the next, is
-// in doubt.
-template <int SLOTS, bool CHECK>
-__device__ __forceinline__ bool pick(int (&key)[SLOTS], int top, Doubt doubt, int& id) {
-  const int lane = threadIdx.x % 64;
-  float prev = __builtin_inff();
+// The top largest keys, equal ones from the lowest expert on: lane j < top of
+// the team gets the j-th's expert (-1: none left); so do lanes up to count where
+// the set of the first top is not sure but that of the first count is.
+//
+// A key's last bits (as many as number the registers) give way to its
+// register's number, counted down.  So the keys of a lane differ, and what a lane
+// has left are those below the last one taken from it: its largest is found
+// by a subtraction and half a minimum each, nothing is marked as taken, and the
+// round's key names its register.  For keys that then agree in the bits above
+// (CHECK: that doubt says may be either way round) the order is not known.
+// exact: those bits said nothing, so keys that agree are equal.
+template <int SLOTS>
+constexpr uint32_t slot_bits() {
+  uint32_t n = 0;
+  while ((1 << n) < SLOTS) n++;
+  return n;
+}
+enum : int { SURE = 0, ORDER = 1, CHOICE = 2 };  // pick's doubt: none, the order of the first count alone, which they are
+template <int TEAM, int SLOTS, bool CHECK>
+__device__ __forceinline__ int pick(const uint32_t (&given)[SLOTS], int top, Doubt doubt, bool exact, int& id, int& count) {
+  constexpr uint32_t kMask = (1u << slot_bits<SLOTS>()) - 1;
+  const int lane = threadIdx.x % TEAM;
+  uint32_t key[SLOTS], below = 0xFFFFFFFFu, best, m = kOff, mine = kOff;
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) key[s] = given[s] == kOff ? kOff : (given[s] & ~kMask) | (kMask - s);
   id = -1;
-  for (int j = 0; j < top + (CHECK ? 1 : 0); j++) {
-    int best = key[0];
+  count = top;
+  auto largest = [&] {
+    // distance from `below` down to the nearest key under it; one that is not under it is further than any that is
+    uint32_t near = below - 1;
 #pragma unroll
-    for (int s = 1; s < SLOTS; s++) best = max(best, key[s]);
-    const int m = wave_max_key(best);
-    if (m == kOff) return true;
-    if constexpr (CHECK) {
-      const float f = of_key(m);
-      if (j > 0 && doubt(prev, f)) return false;
-      prev = f;
-      if (j == top) return true;
+    for (int s = 0; s < SLOTS; s++) near = min(near, below - 1 - key[s]);
+    best = below - 1 - near;
+    return team_max<TEAM>(best);
+  };
+  auto take = [&](int j) {
+    const int l = first_lane<TEAM>(best == m);
+    if (lane == l && m != kOff) below = m;
+    if (lane == j) {
+      mine = m;
+      id = m == kOff ? -1 : l + TEAM * (int)(kMask - (m & kMask));
     }
-    int won = -1;
-#pragma unroll
-    for (int s = 0; s < SLOTS; s++) {
-      if (won < 0) {
-        const unsigned long long at = __ballot(key[s] == m);
-        if (at) {
-          const int l = __ffsll((long long)at) - 1;
-          won = 64 * s + l;
-          if (lane == l) key[s] = kOff;
-        }
-      }
-    }
-    if (lane == j) id = won;
+  };
+  for (int j = 0; j < top; j++) {
+    m = largest();
+    take(j);
   }
-  return true;
+  if (!CHECK && exact) return SURE;
+  auto open = [&](uint32_t a, uint32_t b) {  // a the larger
+    if (b == kOff) return false;
+    return CHECK ? doubt(of_key(a & ~kMask), of_key(b & ~kMask)) : ((a ^ b) & ~kMask) == 0;
+  };
+  uint32_t next = largest();
+  bool edge = open(m, next);
+  // where the last and the next are in doubt, up to four more, until two are not
+  for (; __ballot(edge) && count < TEAM && count < top + 4; count++) {
+    m = next;
+    take(count);
+    next = largest();
+    edge = edge && open(m, next);
+  }
+  // each lane's key against the one before it (wave_shr 1, or within rows of 16)
+  const uint32_t before = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, TEAM == 64 ? 0x138 : 0x111, 0xF, 0xF, false);
+  const bool here = lane > 0 && lane < count && open(before, mine);
+  return edge ? CHOICE : team_max<TEAM>(here ? 1 : 0) ? ORDER : SURE;
 }
 
 // Two largest of the values seen.
@@ -127,125 +202,221 @@ struct Two {
   __device__ __forceinline__ T value(int group_top) const { return group_top == 2 && b > -__builtin_inf() ? a + b : a; }
 };
 
-// Lane g step's value of group g, for g < groups: those kept, as a mask of lanes.
-template <typename T>
-__device__ __forceinline__ unsigned long long kept_groups(T v, int groups, int step, int top_groups) {
-  const int lane = threadIdx.x % 64, g = lane / step;
-  int rank = 0;
-  for (int o = 0; o < groups; o++) {
-    const T u = __shfl(v, o * step);
-    rank += u > v || (u == v && o < g);
-  }
-  return __ballot(g < groups && v > -__builtin_inf() && rank < top_groups);
+// The groups of a lane's experts: (e + 0.5) / per in fp32 is off by less than
+// 2^-10 / per, and no nearer to a whole number than 0.5 / per.
+template <int TEAM, int SLOTS>
+__device__ __forceinline__ void groups_of(float inv_per, int (&group)[SLOTS]) {
+  const float first = ((float)(int)(threadIdx.x % TEAM) + 0.5f) * inv_per;
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) group[s] = (int)__builtin_fmaf((float)(TEAM * s), inv_per, first);
 }
 
-// Expert e's group; `magic` is 2^32 / per rounded up (e and per are at most 4096).
-__device__ __forceinline__ int group_of(int e, unsigned long long magic) { return (int)((unsigned)e * magic >> 32); }
+// How groups are spread: 2^shift lanes of the team share one (one where there
+// are more than half as many as lanes); a lane's i-th group is i TEAM / 2^shift
+// past its first.  In LDS a token has its groups' values, `quads` of four, then
+// its scores, a row of per or per + 1 for each group: odd, so that the rows start
+// in different banks (odd_mask: -1 where one is added); then a place that is
+// written only.
+struct Spread {
+  int per, odd_mask, quads, shift, size;  // size: numbers that a token takes, a multiple of four
+  float inv_per;
+};
+// Scores into their places.
+template <int TEAM, int SLOTS, typename T, typename F>
+__device__ __forceinline__ void lay_out(const RouteArgs& a, const Spread& sp, const int (&group)[SLOTS], T* mine, F score) {
+  const int lane = threadIdx.x % TEAM;
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) {
+    const int e = lane + TEAM * s, at = 4 * sp.quads + e + (group[s] & sp.odd_mask);
+    mine[e < a.experts ? at : sp.size - 1] = score(s);
+  }
+}
 
-// The choice with all scores in fp64.
+// The groups kept, as a mask (bit g, the same in the team's lanes), from the
+// team's scores at[s] in `mine`, which no other team touches.  For the lane's
+// own groups `least` and `most` become the smallest value kept and the largest
+// dropped.
+template <int TEAM, typename T>
+__device__ __forceinline__ unsigned long long keep_groups(const RouteArgs& a, const Spread& sp, T* mine, T& least,
+                                                          T& most) {
+  typedef T T4 __attribute__((ext_vector_type(4)));
+  const int wlane = threadIdx.x % 64, lane = wlane % TEAM;
+  const T off = -__builtin_inf();
+  const T* scores = mine + 4 * sp.quads;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const int step = 1 << sp.shift, stride = TEAM >> sp.shift, rows = 4 * sp.quads, pitch = sp.per - sp.odd_mask;
+  const int part = lane & (step - 1);
+  for (int g0 = 0; g0 < rows; g0 += stride) {
+    const int g = g0 + (lane >> sp.shift);
+    const T* row = scores + min(g, a.groups - 1) * pitch;
+    Two<T> t{off, off};
+    for (int i = part; i - part < sp.per; i += 8 * step) {  // eight in flight
+      T v[8];
+#pragma unroll
+      for (int u = 0; u < 8; u++) v[u] = row[min(i + u * step, sp.per - 1)];
+#pragma unroll
+      for (int u = 0; u < 8; u++) t.add(i + u * step < sp.per ? v[u] : off);
+    }
+    for (int o = 1; o < step; o *= 2) t.join(__shfl_xor(t.a, o), __shfl_xor(t.b, o));
+    if (g < rows && part == 0) mine[g] = g < a.groups ? t.value(a.group_top) : off;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  unsigned long long kept = 0;
+  least = __builtin_inf();
+  most = off;
+  for (int g0 = 0; g0 < a.groups; g0 += TEAM) {
+    const int g = g0 + lane;
+    const T v = g < a.groups ? mine[g] : off;
+    int rank = 0;
+#pragma unroll 4
+    for (int o = 0; o < rows; o += 4) {
+      const T4 u = *reinterpret_cast<const T4*>(mine + o);
+#pragma unroll
+      for (int i = 0; i < 4; i++) rank += o + i < g ? u[i] >= v : u[i] > v;
+    }
+    const bool is = v > off && rank < a.top_groups;
+    if (is) least = fmin(least, v);
+    else most = fmax(most, v);
+    unsigned long long bits = __ballot(is);
+    if constexpr (TEAM < 64) bits = bits >> (wlane - lane) & ((1ull << TEAM) - 1);
+    kept |= bits << g0;
+  }
+  return kept;
+}
+__device__ __forceinline__ bool is_kept(unsigned long long kept, int g) {
+  return (g & 32 ? (uint32_t)(kept >> 32) : (uint32_t)kept) >> (g & 31) & 1;
+}
+
+// The chosen of a team in their true order (their set is right): each lane's
+// logit, or sigmoid's c in fp64, and its place among them.  (A softmax's c needs
+// every logit: choose64.)
+template <int TEAM, int DT>
+__device__ __forceinline__ int order64(const RouteArgs& a, int64_t row, int id, int count) {
+  const int lane = threadIdx.x % TEAM;
+  double c = -__builtin_inf();
+  if (id >= 0) {
+    c = (double)logit_at<DT>(a.logits, row + id);
+    if (a.bias) c = 1.0 / (1.0 + exp(-c)) + (double)a.bias[id];
+  }
+  int place = 0;
+  for (int j = 0; j < count; j++) {
+    const double u = __shfl(c, j, TEAM);
+    const int other = __shfl(id, j, TEAM);
+    place += u > c || (u == c && other < id);
+  }
+  const int to = id < 0 ? lane : place;  // (those without an expert come last already)
+  return __builtin_amdgcn_ds_permute(4 * (int)(threadIdx.x % 64 - lane + to), id);
+}
+
+// The choice for one token with all scores in fp64, by the whole wavefront;
+// `mine` has room for a token's scores.
 template <int DT, int SLOTS>
-__device__ __attribute__((noinline)) int choose64(const RouteArgs& a, int64_t row, unsigned long long magic) {
+__device__ __forceinline__ int choose64(const RouteArgs& a, int64_t row, const Spread& sp, double* mine) {
   const int lane = threadIdx.x % 64;
   const double off = -__builtin_inf();
-  double c[SLOTS];
-  double m = off, sum = 0.0;
-  if (a.score == SCORE_SOFTMAX) {
-#pragma unroll 1
-    for (int e = lane; e < a.experts; e += 64) m = fmax(m, (double)logit_at<DT>(a.logits, row + e));
-    for (int o = 1; o < 64; o *= 2) m = fmax(m, __shfl_xor(m, o));
-#pragma unroll 1
-    for (int e = lane; e < a.experts; e += 64) sum += exp((double)logit_at<DT>(a.logits, row + e) - m);
-    for (int o = 1; o < 64; o *= 2) sum += __shfl_xor(sum, o);
+  const bool softmax = a.score == SCORE_SOFTMAX;
+  auto larger = [](double x, double y) { return fmax(x, y); };
+  double c[SLOTS], m = off, sum = 1.0, part = 0.0;
+  float l[SLOTS];
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) l[s] = logit_at<DT>(a.logits, row + min(lane + 64 * s, a.experts - 1));
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) l[s] = lane + 64 * s < a.experts ? l[s] : -__builtin_inff();
+  if (softmax) {
+#pragma unroll
+    for (int s = 0; s < SLOTS; s++) m = fmax(m, (double)l[s]);
+    m = wave_fold(m, larger);
   }
 #pragma unroll
   for (int s = 0; s < SLOTS; s++) {
-    const int e = lane + 64 * s;
-    c[s] = off;
-    if (e < a.experts) {
-      const double l = (double)logit_at<DT>(a.logits, row + e);
-      const double p = a.score == SCORE_SOFTMAX ? exp(l - m) / sum : 1.0 / (1.0 + exp(-l));
-      const double v = p + (a.bias ? (double)a.bias[e] : 0.0);
-      if (l > off && v > off) c[s] = v;
-    }
+    c[s] = exp(softmax ? (double)l[s] - m : -(double)l[s]);
+    part += c[s];
+  }
+  if (softmax) sum = wave_fold(part, [](double x, double y) { return x + y; });
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) {
+    const double v = (softmax ? c[s] / sum : 1.0 / (1.0 + c[s])) +
+                     (a.bias ? (double)a.bias[min(lane + 64 * s, a.experts - 1)] : 0.0);
+    c[s] = l[s] > -__builtin_inff() && v > off ? v : off;  // (a NaN is off)
   }
   if (a.groups > 1) {
-    double value = off;
-    for (int g = 0; g < a.groups; g++) {
-      Two<double> t{off, off};
+    int group[SLOTS];
+    groups_of<64>(sp.inv_per, group);
+    lay_out<64>(a, sp, group, mine, [&](int s) { return c[s]; });
+    double least, most;
+    Spread wide = sp;
+    wide.shift = 0;
+    while ((2 << wide.shift) * a.groups <= 64) wide.shift++;
+    const unsigned long long kept = keep_groups<64>(a, wide, mine, least, most);
 #pragma unroll
-      for (int s = 0; s < SLOTS; s++)
-        if (group_of(lane + 64 * s, magic) == g) t.add(c[s]);
-      for (int o = 1; o < 64; o *= 2) t.join(__shfl_xor(t.a, o), __shfl_xor(t.b, o));
-      if (lane == g) value = t.value(a.group_top);
-    }
-    const unsigned long long kept = kept_groups(value, a.groups, 1, a.top_groups);
-#pragma unroll
-    for (int s = 0; s < SLOTS; s++) {
-      const int e = lane + 64 * s;
-      if (e < a.experts && !(kept >> group_of(e, magic) & 1)) c[s] = off;
-    }
+    for (int s = 0; s < SLOTS; s++)
+      if (!is_kept(kept, group[s])) c[s] = off;
   }
   if (!a.bias) {
 #pragma unroll
     for (int s = 0; s < SLOTS; s++)
-      if (c[s] > off) c[s] = (double)logit_at<DT>(a.logits, row + lane + 64 * s);
+      if (c[s] > off) c[s] = (double)l[s];
   }
   int id = -1;
   for (int j = 0; j < a.top; j++) {
     double best = c[0];
 #pragma unroll
     for (int s = 1; s < SLOTS; s++) best = fmax(best, c[s]);
-    for (int o = 1; o < 64; o *= 2) best = fmax(best, __shfl_xor(best, o));
+    best = wave_fold(best, larger);
     if (best == off) break;
-    int won = -1;
+    uint32_t last = 0;  // 4096 less the lowest expert with it
 #pragma unroll
-    for (int s = 0; s < SLOTS; s++) {
-      const unsigned long long at = __ballot(c[s] == best);
-      if (won < 0 && at) {
-        const int l = __ffsll((long long)at) - 1;
-        won = 64 * s + l;
-        if (lane == l) c[s] = off;
-      }
-    }
+    for (int s = SLOTS - 1; s >= 0; s--) last = c[s] == best ? 4096 - 64 * s - lane : last;
+    const int won = 4096 - (int)team_max<64>(last);
+#pragma unroll
+    for (int s = 0; s < SLOTS; s++) c[s] = won - lane == 64 * s ? off : c[s];
     if (lane == j) id = won;
   }
   return id;
 }
 
-constexpr int kWaves = 4;  // tokens of a workgroup (two where the groups' scores would not fit 64 KB of LDS)
+constexpr int kWaves = 4;  // wavefronts of a workgroup (fewer where the groups' scores would not fit)
+constexpr size_t kMostLds = 64 << 10;
 
-template <int DT, int SLOTS>
-__global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, int pitch, int step, unsigned long long magic) {
-  extern __shared__ float shared_scores[];  // groups rows of `pitch` for each wavefront
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t token = (int64_t)blockIdx.x * (blockDim.x / 64) + wave;
-  if (token >= a.tokens) return;  // (no barrier below)
+template <int DT, int TEAM, int SLOTS>
+__global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread sp) {
+  extern __shared__ __attribute__((aligned(32))) double shared_scores[];
+  constexpr int kTeams = 64 / TEAM;  // tokens of a wavefront
+  const int wlane = threadIdx.x % 64, wave = threadIdx.x / 64, lane = wlane % TEAM, team = wlane / TEAM;
+  const int64_t first = ((int64_t)blockIdx.x * (blockDim.x / 64) + wave) * kTeams, token = first + team;
+  if (first >= a.tokens) return;  // (no barrier below)
+  const bool there = token < a.tokens, softmax = a.score == SCORE_SOFTMAX;
   const int64_t row = token * a.experts;
   const float ninf = -__builtin_inff();
-  float l[SLOTS];
+  float l[SLOTS], b[SLOTS];
   bool wrong = false;
-  int top_key = kOff;
+  uint32_t top_key = kOff;
+  // Every lane loads, those past the row's end its last logit: a load under a
+  // condition would be waited for before the next.
+  const int64_t at = (there ? token : a.tokens - 1) * a.experts;
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) l[s] = logit_at<DT>(a.logits, at + min(lane + TEAM * s, a.experts - 1));
+#pragma unroll
+  for (int s = 0; s < SLOTS; s++) b[s] = 0.0f;
+  if (a.bias) {
+#pragma unroll
+    for (int s = 0; s < SLOTS; s++) b[s] = a.bias[min(lane + TEAM * s, a.experts - 1)];
+  }
 #pragma unroll
   for (int s = 0; s < SLOTS; s++) {
-    const int e = lane + 64 * s;
-    l[s] = e < a.experts ? logit_at<DT>(a.logits, row + e) + 0.0f : ninf;
-    wrong |= l[s] != l[s] || (a.score == SCORE_SOFTMAX && l[s] == __builtin_inff());
+    l[s] = there && lane + TEAM * s < a.experts ? l[s] + 0.0f : ninf;
+    wrong |= l[s] != l[s] || (softmax && l[s] == __builtin_inff());
     top_key = max(top_key, l[s] > ninf ? key_of(l[s]) : kOff);
   }
-  if (__ballot(wrong)) {
-    if (lane < a.top) {
-      a.ids[token * a.top + lane] = -1;
-      a.weights[token * a.top + lane] = __builtin_nanf("");
-    }
-    return;
-  }
-  const bool softmax = a.score == SCORE_SOFTMAX;
-  // with one key a group the group's order is its logit's
+  wrong = team_max<TEAM>(wrong ? 1 : 0) != 0;
+  // with one score of each group the groups' order is that of the logits too
   const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
   float m = 0.0f, sum = 1.0f;  // softmax: the largest logit, the sum of exp(l - m)
-  if (softmax) m = of_key(wave_max_key(top_key));
-  int key[SLOTS];
-  Doubt doubt{0.0f, 0.0f};
+  if (softmax) m = of_key(team_max<TEAM>(top_key));
+  uint32_t key[SLOTS];
+  Doubt doubt{0.0f, 0.0f}, keys_doubt = doubt;
   if (by_logit) {
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) key[s] = l[s] > ninf ? key_of(l[s]) : kOff;
@@ -254,72 +425,75 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, int pit
     float p[SLOTS], part = 0.0f;
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) {
-      p[s] = l[s] > ninf ? exp_near(softmax ? l[s] - m : -l[s]) : 0.0f;
+      p[s] = __builtin_amdgcn_exp2f((softmax ? l[s] - m : -l[s]) * kLog2eHi);  // (-inf - m: 0; no expert on: NaN, not used)
       part += p[s];
     }
-    if (softmax) sum = wave_sum(part);
+    if (softmax) sum = team_sum<TEAM>(part);
     if (!by_logit) {
-      const float inv = 1.0f / sum;
+      const float inv = softmax ? 1.0f / sum : 1.0f;
       doubt = Doubt{softmax ? (SLOTS > 16 ? 0x1p-15f : 0x1p-17f) * inv : 0x1p-20f, 0x1p-22f};
+      keys_doubt = Doubt{doubt.abs, 0x1p-22f + (1 << slot_bits<SLOTS>()) * 0x1p-23f};
 #pragma unroll
       for (int s = 0; s < SLOTS; s++) {
-        const int e = lane + 64 * s;
-        float c = softmax ? p[s] * inv : __builtin_amdgcn_rcpf(1.0f + p[s]);
-        if (a.bias && e < a.experts) c += a.bias[e];
+        const float c = (softmax ? p[s] * inv : __builtin_amdgcn_rcpf(1.0f + p[s])) + b[s];
         key[s] = l[s] > ninf && c > ninf ? key_of(c) : kOff;
       }
     }
   }
-  bool sure = true;
+  // the wavefront's LDS: kTeams tokens in fp32, or one in fp64
+  double* const wave_scores = shared_scores + wave * sp.size * (kTeams > 2 ? kTeams / 2 : 1);
+  int open = SURE;
   if (a.groups > 1) {
-    float* mine = shared_scores + wave * a.groups * pitch;
-    const int per = a.experts / a.groups;
-    int at[SLOTS];
-#pragma unroll
-    for (int s = 0; s < SLOTS; s++) {
-      const int e = lane + 64 * s, g = group_of(e, magic);
-      at[s] = g;
-      if (e < a.experts) mine[g * pitch + e - g * per] = key[s] == kOff ? ninf : of_key(key[s]);
-    }
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const int g = lane / step;
-    Two<float> t{ninf, ninf};
-    if (g < a.groups)
-      for (int i = lane % step; i < per; i += step) t.add(mine[g * pitch + i]);
-    for (int o = 1; o < step; o *= 2) t.join(__shfl_xor(t.a, o), __shfl_xor(t.b, o));
-    const float value = t.value(a.group_top);
-    const unsigned long long kept = kept_groups(value, a.groups, step, a.top_groups);
-    if (!by_logit && a.top_groups < a.groups) {
-      const bool is = kept >> lane & 1;
-      const int least = wave_max_key(is ? ~key_of(value) : kOff);  // ~: the order turned round
-      const int most = wave_max_key(!is && g < a.groups && value > ninf ? key_of(value) : kOff);
-      if (least != kOff && most != kOff) sure = !doubt(of_key(~least), of_key(most));
+    float* const mine = reinterpret_cast<float*>(wave_scores) + team * sp.size;
+    int group[SLOTS];
+    groups_of<TEAM>(sp.inv_per, group);
+    lay_out<TEAM>(a, sp, group, mine, [&](int s) { return key[s] == kOff ? ninf : of_key(key[s]); });
+    float least, most;
+    const unsigned long long kept = keep_groups<TEAM>(a, sp, mine, least, most);
+    if (!by_logit) {
+      least = -of_key(team_max<TEAM>(key_of(-least)));
+      most = of_key(team_max<TEAM>(key_of(most)));
+      if (most != ninf && doubt(least, most)) open = CHOICE;
     }
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) {
-      if (!(kept >> (at[s] * step & 63) & 1)) key[s] = kOff;
-      else if (!a.bias && key[s] != kOff) key[s] = key_of(l[s]);
+      const uint32_t k = a.bias ? key[s] : key_of(l[s]);
+      key[s] = key[s] != kOff && is_kept(kept, group[s]) ? k : kOff;
     }
   }
-  int id = -1;
-  if (sure) sure = a.bias ? pick<SLOTS, true>(key, a.top, doubt, id) : pick<SLOTS, false>(key, a.top, doubt, id);
-  if (!sure) id = choose64<DT, SLOTS>(a, row, magic);
-
+  int id, count;
+  // (16-bit logits end in zeros: 13 of fp16's, for up to 64 registers)
+  open = max(open, a.bias ? pick<TEAM, SLOTS, true>(key, a.top, keys_doubt, false, id, count)
+                          : pick<TEAM, SLOTS, false>(key, a.top, keys_doubt, DT != DT_F32, id, count));
+  if (wrong) open = SURE;
+  if (!(softmax && a.bias) && __ballot(open == ORDER)) {
+    const int ordered = order64<TEAM, DT>(a, row, id, count);
+    if (open == ORDER) {
+      id = ordered;
+      open = SURE;
+    }
+  }
+  for (unsigned long long again = __ballot(open != SURE); again;) {
+    const int t = (__ffsll((long long)again) - 1) / TEAM;
+    const int of = choose64<DT, (SLOTS * TEAM + 63) / 64>(a, (first + t) * a.experts, sp, wave_scores);
+    const int moved = __shfl(of, lane);
+    if (team == t) id = moved;
+    again &= ~(((TEAM < 64 ? 1ull << TEAM : 0ull) - 1) << (t * TEAM));
+  }
   float w = 0.0f;
-  if (lane < a.top && id >= 0) {
+  if (there && lane < a.top && id >= 0) {
     const float v = logit_at<DT>(a.logits, row + id);
     w = softmax ? exp_near(v - m) : 1.0f / (1.0f + exp_near(-v));
   }
-  if (a.renormalise) sum = wave_sum(w);
-  if (lane < a.top) {
-    a.ids[token * a.top + lane] = id;
-    a.weights[token * a.top + lane] = w > 0.0f ? a.scale * (w / sum) : 0.0f;
+  if (a.renormalise) sum = team_sum<TEAM>(w);
+  if (there && lane < a.top) {
+    a.ids[token * a.top + lane] = wrong ? -1 : id;
+    a.weights[token * a.top + lane] = wrong ? __builtin_nanf("") : w > 0.0f ? a.scale * (w / sum) : 0.0f;
   }
 }
 
 // ---------------------------------------------------------------- gradient
-// The same rows: every expert's slope from the softmax's sum, then the chosen
+// One wavefront a token: every expert's slope from the softmax's sum, then the chosen
 // ones' terms added in the order of the choices.
 template <int DT, int SLOTS>
 __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteArgs a) {
@@ -341,14 +515,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteArgs a) {
   float term = 0.0f;  // what the lane's choice adds to its expert's
   if (__ballot(id >= 0)) {
     if (softmax && !a.renormalise) {
-      int top_key = kOff;
+      uint32_t top_key = kOff;
+#pragma unroll
+      for (int s = 0; s < SLOTS; s++) d[s] = logit_at<DT>(a.logits, row + min(lane + 64 * s, a.experts - 1));
 #pragma unroll
       for (int s = 0; s < SLOTS; s++) {
-        const int e = lane + 64 * s;
-        d[s] = e < a.experts ? logit_at<DT>(a.logits, row + e) + 0.0f : -__builtin_inff();
+        d[s] = lane + 64 * s < a.experts ? d[s] + 0.0f : -__builtin_inff();
         top_key = max(top_key, d[s] > -__builtin_inff() ? key_of(d[s]) : kOff);
       }
-      const float m = of_key(wave_max_key(top_key));
+      const float m = of_key(team_max<64>(top_key));
       float part = 0.0f;
 #pragma unroll
       for (int s = 0; s < SLOTS; s++) {
@@ -362,7 +537,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteArgs a) {
 #pragma unroll
       for (int s = 0; s < SLOTS; s++) d[s] = d[s] * inv * -mean;
     } else if (softmax) {
-      const float m = of_key(wave_max_key(id >= 0 && v > -__builtin_inff() ? key_of(v + 0.0f) : kOff));
+      const float m = of_key(team_max<64>(id >= 0 && v > -__builtin_inff() ? key_of(v + 0.0f) : kOff));
       const float e = id >= 0 && v > -__builtin_inff() ? exp_near(v - m) : 0.0f;
       const float sum = wave_sum(e), share = sum > 0.0f ? e / sum : 0.0f;
       term = share * (g - wave_sum(share * g));
@@ -393,17 +568,15 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteArgs a) {
   }
 }
 
-template <typename F>
-hipError_t with_slots(int experts, F f) {
-  using std::integral_constant;
-  if (experts <= 64) return f(integral_constant<int, 1>());
-  if (experts <= 128) return f(integral_constant<int, 2>());
-  if (experts <= 256) return f(integral_constant<int, 4>());
-  if (experts <= 512) return f(integral_constant<int, 8>());
-  if (experts <= 1024) return f(integral_constant<int, 16>());
-  if (experts <= 2048) return f(integral_constant<int, 32>());
-  return f(integral_constant<int, 64>());
-}
+template <int TEAM>
+struct Slots {
+  // f(SLOTS) for the fewest of a few sizes that hold the experts
+  template <int FIRST, int... REST, typename F>
+  static hipError_t call(int experts, F f) {
+    if (sizeof...(REST) == 0 || experts <= FIRST * TEAM) return f(std::integral_constant<int, FIRST>());
+    if constexpr (sizeof...(REST) > 0) return call<REST...>(experts, f);
+  }
+};
 template <typename F>
 hipError_t with_logits(int dtype, F f) {
   using std::integral_constant;
@@ -418,16 +591,30 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
   if (a.tokens < 1 || a.experts < 1 || a.experts > 4096 || a.top < 1 || a.top > 64 || a.groups < 1 || a.groups > 64 ||
       a.experts % a.groups != 0)
     return hipErrorInvalidValue;
-  const int per = a.experts / a.groups, pitch = per | 1;  // odd: the lanes' rows start in different banks
-  int step = 1;  // lanes of a group
-  while (2 * step * a.groups <= 64) step *= 2;
-  const int waves = a.groups > 1 && a.experts > 2048 ? 2 : kWaves;
-  const size_t lds = a.groups > 1 ? (size_t)waves * a.groups * pitch * sizeof(float) : 0;
-  const unsigned long long magic = ((1ull << 32) + per - 1) / per;
+  const int per = a.experts / a.groups;
+  const bool small = a.experts <= 256 && a.top <= 16;
+  const int team = small ? 16 : 64, teams = 64 / team;
+  Spread sp{per, per % 2 ? 0 : -1, (a.groups + 3) / 4, 0, 0, 1.0f / (float)per};
+  sp.size = (4 * sp.quads + a.groups * (per - sp.odd_mask) + 4) / 4 * 4;
+  while ((2 << sp.shift) * a.groups <= team) sp.shift++;
+  int waves = kWaves;
+  size_t lds = 0;
+  if (a.groups > 1) {
+    const size_t each = (size_t)sp.size * sizeof(double) * (teams > 2 ? teams / 2 : 1);
+    while (waves > 1 && waves * each > kMostLds) waves /= 2;
+    lds = waves * each;
+  }
+  const int64_t tokens = (int64_t)waves * teams;
+  const unsigned blocks = (unsigned)((a.tokens + tokens - 1) / tokens);
   return with_logits(a.dtype, [&](auto DT_) {
-    return with_slots(a.experts, [&](auto SLOTS_) {
-      route_kernel<decltype(DT_)::value, decltype(SLOTS_)::value>
-          <<<(unsigned)((a.tokens + waves - 1) / waves), 64 * waves, lds, s>>>(a, pitch, step, magic);
+    constexpr int DT = decltype(DT_)::value;
+    if (small)
+      return Slots<16>::call<1, 2, 4, 6, 8, 10, 12, 16>(a.experts, [&](auto SLOTS_) {
+        route_kernel<DT, 16, decltype(SLOTS_)::value><<<blocks, 64 * waves, lds, s>>>(a, sp);
+        return hipGetLastError();
+      });
+    return Slots<64>::call<1, 4, 8, 16, 64>(a.experts, [&](auto SLOTS_) {
+      route_kernel<DT, 64, decltype(SLOTS_)::value><<<blocks, 64 * waves, lds, s>>>(a, sp);
       return hipGetLastError();
     });
   });
@@ -436,7 +623,7 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
 hipError_t launch_moe_route_grad(const RouteArgs& a, hipStream_t s) {
   if (a.tokens < 1 || a.experts < 1 || a.experts > 4096 || a.top < 1 || a.top > 64) return hipErrorInvalidValue;
   return with_logits(a.dtype, [&](auto DT_) {
-    return with_slots(a.experts, [&](auto SLOTS_) {
+    return Slots<64>::call<1, 2, 3, 4, 8, 16, 64>(a.experts, [&](auto SLOTS_) {
       route_grad_kernel<decltype(DT_)::value, decltype(SLOTS_)::value>
           <<<(unsigned)((a.tokens + kWaves - 1) / kWaves), 64 * kWaves, 0, s>>>(a);
       return hipGetLastError();
