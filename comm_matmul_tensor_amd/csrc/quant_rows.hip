@@ -3,8 +3,7 @@
 //   a = max |x|, scale = a / 127, code = rint(x / scale); out = act(code scale)
 //
 // Bound by HBM: a row is read once, kept in registers across its maximum and
-// its codes written once.  The division is the IEEE one, so that the codes are
-// those of the formula.
+// its codes written once.
 //
 // Per 128 columns the 16 lanes that hold a group's chunks of 8 find its
 // maximum by DPP; nothing else depends on the row, so threads take chunks of
@@ -26,14 +25,42 @@ __device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
   for (int e = 0; e < 8; e++) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);  // (a NaN is the largest)
   return m;
 }
-// A scale that is 0, NaN or infinite gives codes 0.
-__device__ __forceinline__ u32x2 codes_of(const float (&x)[8], float scale) {
+// What a group's codes need of its scale.
+struct Divisor {
+  float scale, inverse;
+  bool usable, fast;
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s), inverse(1.0f / s) {
+    usable = s > 0.0f && s < __builtin_inff();  // a scale that is 0, NaN or infinite gives codes 0
+    fast = usable && s > 0x1p-100f;             // the inverse neither overflows nor loses bits
+  }
+};
+// The codes are those of the IEEE quotient, found without dividing: x times the
+// inverse is off from it by 127 (2^-24 + 2^-24) at most, so both round to the
+// same whole number unless that product lies within 2^-14 of a half; only then
+// (one value in 8000) are the eight divided.  Added to 1.5 2^23, the product
+// rounds to the whole number in the sum's last bits, its low byte the code.
+__device__ __forceinline__ u32x2 codes_of(const float (&x)[8], const Divisor& d) {
+  constexpr float kRound = 12582912.0f;
   u32x2 r = {0u, 0u};
-  if (!(scale > 0.0f && scale < __builtin_inff())) return r;
+  if (!d.usable) return r;
+  float t[8], far = 1.0f;
+  if (d.fast) {
+    far = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const float q = fminf(fmaxf(x[e] / scale, -127.0f), 127.0f);
-    r[e / 4] |= ((uint32_t)(int)__builtin_rintf(q) & 0xFFu) << (8 * (e & 3));
+    for (int e = 0; e < 8; e++) {
+      t[e] = __builtin_fmaf(x[e], d.inverse, kRound);
+      far = fmaxf(far, __builtin_fabsf(__builtin_fmaf(x[e], d.inverse, -(t[e] - kRound))));
+    }
+  }
+  if (far > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) t[e] = x[e] / d.scale + kRound;
+  }
+#pragma unroll
+  for (int w = 0; w < 2; w++) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * w + 1]), __float_as_uint(t[4 * w]), 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * w + 3]), __float_as_uint(t[4 * w + 2]), 0x04000C0Cu);
+    r[w] = lo | hi;
   }
   return r;
 }
@@ -48,23 +75,17 @@ __device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t cols
   }
 }
 
-// Threads of a row for `chunks` chunks: the power of two from `least` to 256
-// that leaves the fewest idle in a row's last turn, the larger of two alike.
+// Threads of a row of `chunks` chunks: the most, up to 256, that leave no more
+// than an eighth of them idle over the row's turns, `least` at least.
 int row_threads(int64_t chunks, int least) {
   int best = least;
-  int64_t waste = INT64_MAX;
-  for (int t = least; t <= 256; t *= 2) {
-    const int64_t w = (chunks + t - 1) / t * t - chunks;
-    if (w <= waste) {
-      waste = w;
-      best = t;
-    }
-    if (t >= chunks) break;
-  }
+  for (int t = least; t <= 256; t *= 2)
+    if ((chunks + t - 1) / t * t - chunks <= chunks / 8) best = t;
   return best;
 }
 
 // ---------------------------------------------------------------- per 128 columns
+constexpr int kFlight = 4;  // chunks that a thread loads before it uses one
 template <int DT, bool VEC>
 __global__ __launch_bounds__(256) void quant_groups(CodeArgs a, int tpr) {
   const int64_t row = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
@@ -73,16 +94,24 @@ __global__ __launch_bounds__(256) void quant_groups(CodeArgs a, int tpr) {
   int8_t* codes = a.codes + row * a.cols;
   float* scales = a.scale + row * scales_of(a.cols, 128);
   const int64_t last = (a.cols + 127) / 128 * 128;  // a group's lanes all take part
-#pragma unroll 4
-  for (int64_t c = 8 * (int64_t)(threadIdx.x % tpr); c < last; c += 8 * tpr) {
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (c < a.cols) v = load_chunk<VEC>(x, c, a.cols);
-    float f[8];
-    unpack8<DT>(v, f);
-    const float scale = scale_of(max16(top_of(f)));
-    if (c >= a.cols) continue;
-    if (c % 128 == 0) scales[c / 128] = scale;
-    store_codes<VEC>(codes, c, a.cols, codes_of(f, scale));
+  for (int64_t c0 = 8 * (int64_t)(threadIdx.x % tpr); c0 < last; c0 += kFlight * 8 * tpr) {
+    u32x4 v[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; u++) {
+      const int64_t c = c0 + u * 8 * tpr;
+      // (whole rows of chunks: past the end the last one again, so that no load waits for a condition)
+      v[u] = load_chunk<VEC>(x, VEC && c >= a.cols ? a.cols - 8 : c, a.cols);
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; u++) {
+      const int64_t c = c0 + u * 8 * tpr;
+      float f[8];
+      unpack8<DT>(v[u], f);
+      const Divisor d(scale_of(max16(VEC && c >= a.cols ? 0u : top_of(f))));
+      if (c >= a.cols) continue;
+      if (c % 128 == 0) scales[c / 128] = d.scale;
+      store_codes<VEC>(codes, c, a.cols, codes_of(f, d));
+    }
   }
 }
 
@@ -110,14 +139,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void quant_row(CodeArgs a) {
     unpack8<DT>(v[i], f);
     top = max(top, top_of(f));
   }
-  const float scale = scale_of(block_max<WAVES>(top, red));
-  if (t == 0) a.scale[row] = scale;
+  const Divisor d(scale_of(block_max<WAVES>(top, red)));
+  if (t == 0) a.scale[row] = d.scale;
 #pragma unroll
   for (int i = 0; i < NCH; i++) {
     const int64_t c = 8 * (int64_t)(t + i * TPR);
     float f[8];
     unpack8<DT>(v[i], f);
-    if (c < a.cols) store_codes<VEC>(a.codes + row * a.cols, c, a.cols, codes_of(f, scale));
+    if (c < a.cols) store_codes<VEC>(a.codes + row * a.cols, c, a.cols, codes_of(f, d));
   }
 }
 
@@ -133,12 +162,12 @@ __global__ __launch_bounds__(kWide) void quant_wide(CodeArgs a) {
     unpack8<DT>(load_chunk<VEC>(x, c, a.cols), f);
     top = max(top, top_of(f));
   }
-  const float scale = scale_of(block_max<kWide / 64>(top, red));
-  if (threadIdx.x == 0) a.scale[row] = scale;
+  const Divisor d(scale_of(block_max<kWide / 64>(top, red)));
+  if (threadIdx.x == 0) a.scale[row] = d.scale;
   for (int64_t c = 8 * (int64_t)threadIdx.x; c < a.cols; c += 8 * kWide) {
     float f[8];
     unpack8<DT>(load_chunk<VEC>(x, c, a.cols), f);
-    store_codes<VEC>(a.codes + row * a.cols, c, a.cols, codes_of(f, scale));
+    store_codes<VEC>(a.codes + row * a.cols, c, a.cols, codes_of(f, d));
   }
 }
 
@@ -175,19 +204,32 @@ __global__ __launch_bounds__(256) void dequant_kernel(CodeArgs a, int tpr) {
   const int8_t* codes = a.codes_in + row * a.cols;
   const float* scales = a.scale_in + row * scales_of(a.cols, a.group);
   uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ld;
-#pragma unroll 4
-  for (int64_t c = 8 * (int64_t)(threadIdx.x % tpr); c < a.ld; c += 8 * tpr) {
-    float f[8];
-    code_values(load_codes<VEC>(codes, c, a.cols), scales[scale_at(c < a.cols ? c : 0, a.group)], f);
+  for (int64_t c0 = 8 * (int64_t)(threadIdx.x % tpr); c0 < a.ld; c0 += kFlight * 8 * tpr) {
+    u32x2 v[kFlight];
+    float scale[kFlight];
 #pragma unroll
-    for (int e = 0; e < 8; e++) f[e] = VEC || c + e < a.cols ? act_of<ACT>(f[e]) : 0.0f;
-    store_chunk<VEC, true>(out, c, a.ld, pack8<DT>(f));
+    for (int u = 0; u < kFlight; u++) {
+      const int64_t c = c0 + u * 8 * tpr, in = c < a.cols ? c : VEC ? a.cols - 8 : 0;
+      v[u] = load_codes<VEC>(codes, VEC ? in : c, a.cols);
+      scale[u] = scales[scale_at(in, a.group)];
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; u++) {
+      const int64_t c = c0 + u * 8 * tpr;
+      if (c >= a.ld) continue;
+      float f[8];
+      code_values(v[u], scale[u], f);
+#pragma unroll
+      for (int e = 0; e < 8; e++) f[e] = VEC || c + e < a.cols ? act_of<ACT>(f[e]) : 0.0f;
+      store_chunk<VEC, true>(out, c, a.ld, pack8<DT>(f));
+    }
   }
 }
 
 template <int DT, int ACT>
 hipError_t dequant_launch(const CodeArgs& a, hipStream_t s) {
-  const int tpr = row_threads((a.cols + 7) / 8, 1), per = 256 / tpr;
+  const int64_t chunks = (a.cols + 7) / 8;
+  const int tpr = row_threads(chunks, chunks < 8 ? 1 : 8), per = 256 / tpr;
   const unsigned blocks = (unsigned)((a.rows + per - 1) / per);
   if (a.cols % 8 == 0) dequant_kernel<DT, ACT, true><<<blocks, 256, 0, s>>>(a, tpr);
   else dequant_kernel<DT, ACT, false><<<blocks, 256, 0, s>>>(a, tpr);
