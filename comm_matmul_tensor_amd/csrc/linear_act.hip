@@ -39,7 +39,7 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
     }
     return (double)((m + t.bm - 1) / t.bm) * cols * (gmode == BY_K ? (double)groups : 1.0);
   };
-  Plan p{TILE_128X128, 1, k, 0};
+  Plan p{TILE_128X128, 1, k, 0, 0.0};
   const TurnTime* chosen = nullptr;
   double best = 0.0;
   int64_t s = 1;
@@ -63,6 +63,7 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
     }
   }
   p.tile = chosen->tile;
+  p.us = best;
   if (s > 1) {
     p.k_part = ((k + s - 1) / s + kStepK - 1) / kStepK * kStepK;
     p.splits = (int)((k + p.k_part - 1) / p.k_part);

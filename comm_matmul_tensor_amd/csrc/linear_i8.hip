@@ -118,9 +118,29 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_i8_kernel(Product p, int64_
 
 constexpr int64_t kSkinnyRows = 32;
 
+// Wavefronts of a workgroup: 16 while no CU has a second workgroup, and for a
+// very long K (one row, in us, 4 / 16: 4096 x 4096 7.6 / 6.7, 7168 x 4096 9.9 /
+// 7.8 (k x n); 16384 x 8192 31.2 / 28.1, 16384 x 16384 59.8 / 54.9); else 4, whose
+// workgroups start and join sooner (4096 x 28672 25.2 / 27.1, 512 x 20480 5.5 / 6.9,
+// 8192 x 8192 14.0 / 14.9).
 int skinny_waves(int64_t m, int64_t k, int64_t n) {
   const int64_t blocks = (n + 15) / 16;
-  return blocks <= 256 || (blocks > 512 && k >= 4096 && m <= 16) ? 16 : 4;
+  return blocks <= 256 || (k >= 16384 && m <= 16) ? 16 : 4;
+}
+
+// Whether up to 32 rows take this product or tiles, whose workgroups share the
+// rows of x among 64 columns.  Here a CU reads the 16 rows of w and the m of x of
+// each of its workgroups at 36 bytes a ns (16 rows, 16384 x 1024: 17.3 us, tiles
+// 11.3; 32 rows 24.3, 12.1), tiles take their plan's time; neither less than
+// HBM's (tiles at a lower rate: 16 rows of 4096 x 28672 32.5 us, here 36.0; 8
+// rows 32.2, 31.2; 1 row 33.3, 28.1).  16 rows of 4096 x 4096 7.5, tiles 10.1; of 4096 x
+// 7168 10.9, 10.3; 24 rows of 1792 x 7168 8.2, 7.6.
+bool skinny(int64_t m, int64_t k, int64_t n, int64_t groups, const Plan& tiles) {
+  if (groups || m > kSkinnyRows) return false;
+  if (m <= 8) return true;
+  const double bytes = (double)n * (double)k, cus = std::max(1.0, (double)n / 16.0 / 256.0);
+  const double here = std::max((double)(16 + m) * (double)k * cus / 30e3, bytes / 5e6);
+  return here <= std::max(tiles.us, bytes / 4.2e6);
 }
 
 template <int DT, int MF>
@@ -142,16 +162,18 @@ hipError_t launch_skinny(const Product& p, int64_t k, hipStream_t s) {
 // many bytes as the 16-bit ones.
 struct LayoutI8 {
   size_t x, w, partial, total = 0;
-  Plan plan;
+  Plan plan{};
+  bool few;  // the product of few rows
   LayoutI8(int64_t m, int64_t k, int64_t n, int64_t groups) {
     auto take = [&](size_t bytes) {
       const size_t at = total;
       total += up256(bytes);
       return at;
     };
-    const bool skinny = !groups && m <= kSkinnyRows;
-    plan = skinny ? Plan{} : plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups);
-    const bool ragged = k % 16 != 0 && !skinny;
+    if (groups || m > 8) plan = plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups);
+    few = skinny(m, k, n, groups, plan);
+    if (few) plan = Plan{};
+    const bool ragged = k % 16 != 0 && !few;
     x = take(ragged ? (size_t)m * pad16(k) : 0);
     w = take(ragged ? (size_t)std::max<int64_t>(groups, 1) * n * pad16(k) : 0);
     partial = take(plan.partial_bytes);
@@ -177,8 +199,7 @@ hipError_t linear_i8_dt(const LinearI8Args& a, hipStream_t s) {
   p.out = a.out;
   p.act = a.act;
   p.splits = 1;
-  if (!a.groups && a.m <= kSkinnyRows)
-    return a.m <= 16 ? launch_skinny<DT, 1>(p, a.k, s) : launch_skinny<DT, 2>(p, a.k, s);
+  if (at.few) return a.m <= 16 ? launch_skinny<DT, 1>(p, a.k, s) : launch_skinny<DT, 2>(p, a.k, s);
   p.lda = p.ldb = p.k;
   p.b_group = a.n * p.ldb;
   if (a.k % 16) {
@@ -205,14 +226,9 @@ hipError_t linear_i8_dt(const LinearI8Args& a, hipStream_t s) {
 }  // namespace lin
 
 void linear_i8_plan(int64_t m, int64_t k, int64_t n, int64_t groups, int* tile, int* splits) {
-  if (!groups && m <= lin::kSkinnyRows) {
-    *tile = -lin::skinny_waves(m, k, n);
-    *splits = 1;
-    return;
-  }
-  const lin::Plan p = lin::LayoutI8(m, k, n, groups).plan;
-  *tile = p.tile;
-  *splits = p.splits;
+  const lin::LayoutI8 at(m, k, n, groups);
+  *tile = at.few ? -lin::skinny_waves(m, k, n) : (int)at.plan.tile;
+  *splits = at.few ? 1 : at.plan.splits;
 }
 
 size_t linear_i8_workspace(int64_t m, int64_t k, int64_t n, int64_t groups) {

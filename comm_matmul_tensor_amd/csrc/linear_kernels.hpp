@@ -20,6 +20,7 @@ struct Plan {
   int splits;        // parts of K (dense, 128 columns or fewer), each k_part long
   int64_t k_part;
   size_t partial_bytes;
+  double us;         // the time it was chosen for
 };
 // Layout: 0 A K-, B K-contiguous (forward); 1 A K-, B N-contiguous (dx);
 // 2 A M-, B N-contiguous (dw).

@@ -185,8 +185,9 @@ hipError_t quant_launch(const CodeArgs& a, hipStream_t s) {
   const int64_t h = a.cols;
   if (h <= 512) wave(integral_constant<int, 1>());
   else if (h <= 1024) wave(integral_constant<int, 2>());
+  else if (h <= 2048 && a.rows >= 1024) wave(integral_constant<int, 4>());  // 8191 x 1792, there and back: 19.6 us, a workgroup a row 23; 16 x 2048 5.8, 5.3
   else if (h <= 2048) quant_row<DT, 256, 1, VEC><<<(unsigned)a.rows, 256, 0, s>>>(a);
-  else if (h <= 4096) quant_row<DT, 512, 1, VEC><<<(unsigned)a.rows, 512, 0, s>>>(a);
+  else if (h <= 4096) quant_row<DT, 256, 2, VEC><<<(unsigned)a.rows, 256, 0, s>>>(a);  // 8192 x 4096, there and back: 512 threads 43 us, 34
   else if (h <= 8192) quant_row<DT, 512, 2, VEC><<<(unsigned)a.rows, 512, 0, s>>>(a);
   else if (h <= 16384) quant_row<DT, 1024, 2, VEC><<<(unsigned)a.rows, 1024, 0, s>>>(a);
   else if (h <= 32768) quant_row<DT, 1024, 4, VEC><<<(unsigned)a.rows, 1024, 0, s>>>(a);
