@@ -29,7 +29,17 @@ constexpr TurnTime kTurns[] = {{TILE_256X256, 256, 256, 9.0, 1.39}, {TILE_128X25
                                {TILE_128X64, 128, 64, 2.4, 0.27},   {TILE_96X64, 96, 64, 1.2, 0.225},
                                {TILE_64X64, 64, 64, 1.2, 0.18}};
 
-Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_t groups) {
+// Of int8 codes, per step of 128 (one turn: 256 x 256 58.0 us at k = 4096, 128 x
+// 256 34.0, 128 x 128 21.5, 96 x 128 18.4, 128 x 64 14.6, 96 x 64 12.4, 64 x 64 10.8).
+// The steps of 128 x 128 and under are those of many turns, which read 20 TB/s
+// from the L2s and miss there: 4096 x 4096 -> 5000 in five turns 103 us, 95 in three
+// of 128 x 256; 32 experts of 4096 -> 1792, 8191 rows 126 and 112.
+constexpr TurnTime kTurnsI8[] = {{TILE_256X256, 256, 256, 9.5, 1.42}, {TILE_128X256, 128, 256, 5.6, 0.81},
+                                 {TILE_128X128, 128, 128, 4.7, 0.50}, {TILE_96X128, 96, 128, 3.7, 0.39},
+                                 {TILE_128X64, 128, 64, 2.8, 0.28},   {TILE_96X64, 96, 64, 1.6, 0.245},
+                                 {TILE_64X64, 64, 64, 1.2, 0.20}};
+
+Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_t groups, bool i8) {
   const double steps = std::ceil((double)k / (gmode == BY_K ? (double)groups : 1.0) / kStepK);
   auto tiles = [&](const TurnTime& t) {
     const double cols = (double)((n + t.bn - 1) / t.bn);
@@ -43,7 +53,7 @@ Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_
   const TurnTime* chosen = nullptr;
   double best = 0.0;
   int64_t s = 1;
-  for (const TurnTime& t : kTurns) {
+  for (const TurnTime& t : i8 ? kTurnsI8 : kTurns) {
     if (t.tile > TILE_128X128 && gmode == BY_K) break;
     if ((t.bm == 96 && layout == 2) || (t.tile == TILE_128X64 && gmode == BY_ROWS)) continue;
     const double count = tiles(t);

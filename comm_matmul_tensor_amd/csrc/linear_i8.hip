@@ -11,6 +11,9 @@ namespace lin {
 namespace {
 
 int64_t pad16(int64_t v) { return (v + 15) / 16 * 16; }
+// Bytes between padded rows: whole cache lines, so that a step's 128 bytes of a
+// row are one of them (4096 x 4001 -> 5000: 128 us, 141 with rows of 4016).
+int64_t pad128(int64_t v) { return (v + 127) / 128 * 128; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Sixteen codes of a row of k from c (a multiple of 16), zeros past its end.
@@ -157,9 +160,7 @@ hipError_t launch_skinny(const Product& p, int64_t k, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Parts of the workspace, each 256-byte aligned.  The tiled product's K counts
-// pairs of codes, so plan_product's times hold: its steps move and multiply as
-// many bytes as the 16-bit ones.
+// Parts of the workspace, each 256-byte aligned.
 struct LayoutI8 {
   size_t x, w, partial, total = 0;
   Plan plan{};
@@ -170,12 +171,12 @@ struct LayoutI8 {
       total += up256(bytes);
       return at;
     };
-    if (groups || m > 8) plan = plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups);
+    if (groups || m > 8) plan = plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups, true);
     few = skinny(m, k, n, groups, plan);
     if (few) plan = Plan{};
     const bool ragged = k % 16 != 0 && !few;
-    x = take(ragged ? (size_t)m * pad16(k) : 0);
-    w = take(ragged ? (size_t)std::max<int64_t>(groups, 1) * n * pad16(k) : 0);
+    x = take(ragged ? (size_t)m * pad128(k) : 0);
+    w = take(ragged ? (size_t)std::max<int64_t>(groups, 1) * n * pad128(k) : 0);
     partial = take(plan.partial_bytes);
   }
 };
@@ -200,7 +201,7 @@ hipError_t linear_i8_dt(const LinearI8Args& a, hipStream_t s) {
   p.act = a.act;
   p.splits = 1;
   if (at.few) return a.m <= 16 ? launch_skinny<DT, 1>(p, a.k, s) : launch_skinny<DT, 2>(p, a.k, s);
-  p.lda = p.ldb = p.k;
+  p.lda = p.ldb = (a.k % 16 ? pad128(a.k) : a.k) / 2;
   p.b_group = a.n * p.ldb;
   if (a.k % 16) {
     const int64_t matrices = std::max<int64_t>(a.groups, 1);
@@ -208,7 +209,7 @@ hipError_t linear_i8_dt(const LinearI8Args& a, hipStream_t s) {
                 {reinterpret_cast<int8_t*>(ws + at.x), reinterpret_cast<int8_t*>(ws + at.w)},
                 {a.m, matrices * a.n},
                 a.k,
-                pad16(a.k),
+                pad128(a.k),
                 1};
     while (pad.tpr < 256 && 16 * pad.tpr < a.k) pad.tpr *= 2;
     const int64_t per = 256 / pad.tpr, blocks = (a.m + matrices * a.n + per - 1) / per;

@@ -24,7 +24,8 @@ struct Plan {
 };
 // Layout: 0 A K-, B K-contiguous (forward); 1 A K-, B N-contiguous (dx);
 // 2 A M-, B N-contiguous (dw).
-Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_t groups);
+// i8: of codes, k in pairs.
+Plan plan_product(int64_t m, int64_t n, int64_t k, int layout, int gmode, int64_t groups, bool i8 = false);
 
 // The product's splits, k_part, partial, order
 // and epilogue are set here from the plan.
