@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void join_kernel(Product p, int64_t ld, int64_
     i32x4 c = *reinterpret_cast<const i32x4*>(src);
 #pragma unroll 4
     for (int s = 1; s < p.splits; s++) c += *reinterpret_cast<const i32x4*>(src + s * part);
-    const f32x4 sb = load_scales(p.b_scale + col, n, p.n % 4 == 0);
+    const f32x4 sb = load4_any(p.b_scale, col, p.n, p.n % 4 == 0);
     const float sa = p.a_scale[row];
     for (int r = 0; r < 4; r++) v[r] = ((float)c[r] * sa) * sb[r];
   } else {

@@ -318,15 +318,21 @@ __device__ __forceinline__ u32x2 load4(const uint16_t* p, int64_t left, bool qua
   }
   return v;
 }
-__device__ __forceinline__ f32x4 load_scales(const float* p, int64_t left, bool quads) {
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (quads) {
-    if (left > 0) v = *reinterpret_cast<const f32x4*>(p);
-  } else {
+// Four values of a row of n from column c on, each from a column there is (those
+// past the row's end are for columns that are not stored); quads as above.  A
+// load that depends on nothing is not waited for before the next one.
+__device__ __forceinline__ u32x2 load4_any(const uint16_t* row, int64_t c, int64_t n, bool quads) {
+  if (quads) return *reinterpret_cast<const u32x2*>(row + (c < n ? c : n - 4));
+  u32x2 v = {0u, 0u};
 #pragma unroll
-    for (int r = 0; r < 4; r++)
-      if (r < left) v[r] = p[r];
-  }
+  for (int r = 0; r < 4; r++) v[r / 2] |= (uint32_t)row[c + r < n ? c + r : n - 1] << (16 * (r & 1));
+  return v;
+}
+__device__ __forceinline__ f32x4 load4_any(const float* row, int64_t c, int64_t n, bool quads) {
+  if (quads) return *reinterpret_cast<const f32x4*>(row + (c < n ? c : n - 4));
+  f32x4 v;
+#pragma unroll
+  for (int r = 0; r < 4; r++) v[r] = row[c + r < n ? c + r : n - 1];
   return v;
 }
 template <int DT>
@@ -493,7 +499,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
 #pragma unroll
     for (int j = 0; j < FN; j++)
-      rv[j] = load4(residual + row * p.n + col0 + 16 * j, row < m_end ? p.n - col0 - 16 * j : 0, quads);
+      if constexpr (I8) rv[j] = load4_any(residual + (row < m_end ? row : m_end - 1) * p.n, col0 + 16 * j, p.n, quads);
+      else rv[j] = load4(residual + row * p.n + col0 + 16 * j, row < m_end ? p.n - col0 - 16 * j : 0, quads);
   };
   constexpr bool kEarly = FM * FN <= 16;
   u32x2 early[kEarly ? FM : 1][FN];
@@ -564,21 +571,32 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     return reinterpret_cast<u32x2*>((row < BM / 2 ? h0 + row * kPitch : h1 + (row - BM / 2) * kPitch) + col);
   };
   if constexpr (I8) {
-    // (zeros where nothing is stored, and for rows of no group: their sums are 0)
-    f32x4 sb[FN];
+    // z from the sums; all loads are in flight at once
+    if (scaled) {
+      f32x4 sb[FN];
+      u32x2 bv[FN];
+      float sa[FM];
 #pragma unroll
-    for (int j = 0; j < FN; j++) sb[j] = load_scales(b_scale + col0 + 16 * j, scaled ? p.n - col0 - 16 * j : 0, quads);
+      for (int j = 0; j < FN; j++) sb[j] = load4_any(b_scale, col0 + 16 * j, p.n, quads);
 #pragma unroll
-    for (int i = 0; i < FM; i++) {
-      const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
-      const float sa = scaled && row < m_end ? p.a_scale[row] : 0.0f;
+      for (int i = 0; i < FM; i++) {
+        const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
+        sa[i] = p.a_scale[row < m_end ? row : m_end - 1];
+      }
+#pragma unroll
+      for (int j = 0; j < FN; j++) bv[j] = bias ? load4_any(bias, col0 + 16 * j, p.n, quads) : u32x2{0u, 0u};
 #pragma unroll
       for (int j = 0; j < FN; j++) {
-        const i32x4 c = __builtin_bit_cast(i32x4, acc[i][j]);
+        const f32x4 b = widen4<DT>(bv[j]);
 #pragma unroll
-        for (int r = 0; r < 4; r++) acc[i][j][r] = ((float)c[r] * sa) * sb[j][r];
+        for (int i = 0; i < FM; i++) {
+          const i32x4 c = __builtin_bit_cast(i32x4, acc[i][j]);
+#pragma unroll
+          for (int r = 0; r < 4; r++) acc[i][j][r] = ((float)c[r] * sa[i]) * sb[j][r] + b[r];
+        }
       }
-    }
+    }  // (rows of no group: their sums are 0, as z is)
+    bias = nullptr;
   }
   if (bias) {
 #pragma unroll
