@@ -5,7 +5,6 @@
 #include <cmath>
 
 #include "codes.hpp"
-#include "layer8_kernels.hpp"
 #include "linear_kernels.hpp"
 
 namespace mc2 {
@@ -244,19 +243,19 @@ struct DzArgs {
   const int8_t* z_codes;  // EIGHT: z as codes, a scale per 128 columns
   const float* z_scale;
 };
+// Tile (bx, by) of it; red: 256 * 8 numbers, [row of threads][column].
 template <int DT, int ACT, bool VEC, bool EIGHT>
-__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
-  __shared__ float red[256 * 8];  // [row of threads][column]
-  int64_t m0 = (int64_t)blockIdx.x * kDzRows, m_end = a.m;
+__device__ __forceinline__ void dz_tile(const DzArgs& a, unsigned bx, unsigned by, float* red) {
+  int64_t m0 = (int64_t)bx * kDzRows, m_end = a.m;
   if (a.groups > 0) {
-    const RowRange r = find_tile(a.offsets, a.groups, a.m, kDzRows, blockIdx.x);
+    const RowRange r = find_tile(a.offsets, a.groups, a.m, kDzRows, bx);
     if (r.group == a.groups) return;
     m0 = r.begin + r.tile * kDzRows;
     m_end = r.end;
   }
   if (m0 + kDzRows < m_end) m_end = m0 + kDzRows;
   const int tpr = a.tpr, rows = 256 / tpr, rt = threadIdx.x / tpr, ct = threadIdx.x % tpr;
-  const int64_t c0 = (int64_t)blockIdx.y * tpr * 8, c = c0 + 8 * ct;
+  const int64_t c0 = (int64_t)by * tpr * 8, c = c0 + 8 * ct;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < a.n) {
 #pragma unroll 2
@@ -287,7 +286,28 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
   for (int i = threadIdx.x; i < 8 * tpr && c0 + i < a.n; i += 256) {
     float s = red[i];
     for (int r = 1; r < rows; r++) s += red[r * (8 * tpr) + i];
-    a.partial[(int64_t)blockIdx.x * a.n + c0 + i] = s;
+    a.partial[(int64_t)bx * a.n + c0 + i] = s;
+  }
+}
+template <int DT, int ACT, bool VEC>
+__global__ __launch_bounds__(256) void dz_kernel(DzArgs a) {
+  __shared__ float red[256 * 8];
+  dz_tile<DT, ACT, VEC, false>(a, blockIdx.x, blockIdx.y, red);
+}
+// The same from z's codes, and x's codes to 16 bits, whose values the product
+// for dw reads in many tiles: both in one launch, as a batch of some hundred rows
+// is bound by its launches.  The first tiles * cols workgroups are dz's.
+template <int DT, bool VECN, bool VECK>
+__global__ __launch_bounds__(256) void kept_kernel(DzArgs a, unsigned tiles, unsigned cols, int act, CodeArgs x, int tpr) {
+  __shared__ float red[256 * 8];
+  if (blockIdx.x < tiles * cols) {
+    with_act(act, [&](auto ACT_) {
+      dz_tile<DT, decltype(ACT_)::value, VECN, true>(a, blockIdx.x % tiles, blockIdx.x / tiles, red);
+    });
+  } else {
+    with_act(x.act, [&](auto ACT_) {
+      dequant_block<DT, decltype(ACT_)::value, VECK>(x, tpr, blockIdx.x - tiles * cols);
+    });
   }
 }
 
@@ -317,23 +337,35 @@ __global__ __launch_bounds__(256) void dbias_kernel(DzArgs a, int64_t tiles, uin
 
 int64_t dz_tiles(int64_t m, int64_t groups) { return (m + kDzRows - 1) / kDzRows + groups; }
 
+// wide: x's codes to be widened on the way (z is codes then too), or NULL.
 template <int DT>
-hipError_t launch_dz(DzArgs a, int act, void* dbias, hipStream_t s) {
+hipError_t launch_dz(DzArgs a, int act, void* dbias, const CodeArgs* wide, hipStream_t s) {
   a.tpr = 8;
   while (a.tpr < kDzThreads && 8 * a.tpr < a.n) a.tpr *= 2;
   const int64_t tiles = dz_tiles(a.m, a.groups);
   const bool vec = a.n % 8 == 0;
-  if (a.m > 0 && (a.dz || dbias)) {
+  const bool sums = a.dz || dbias;
+  if (a.m > 0 && (wide || (a.z_codes && sums))) {
+    const unsigned cols = sums ? (unsigned)((a.n + 8 * a.tpr - 1) / (8 * a.tpr)) : 0;
+    const CodeArgs x = wide ? *wide : CodeArgs{};
+    const int tpr = wide ? dequant_threads(x.cols) : 1;
+    const unsigned blocks = (unsigned)tiles * cols + (wide ? (unsigned)((x.rows + 256 / tpr - 1) / (256 / tpr)) : 0);
+    auto kept = [&](auto VECN_, auto VECK_) {
+      kept_kernel<DT, decltype(VECN_)::value, decltype(VECK_)::value>
+          <<<blocks, 256, 0, s>>>(a, (unsigned)tiles, cols, act, x, tpr);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    if (vec) x.cols % 8 == 0 ? kept(yes, yes) : kept(yes, no);
+    else x.cols % 8 == 0 ? kept(no, yes) : kept(no, no);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  } else if (a.m > 0 && sums) {
     const dim3 grid((unsigned)tiles, (unsigned)((a.n + 8 * a.tpr - 1) / (8 * a.tpr)));
     with_act(act, [&](auto ACT_) {
       constexpr int ACT = decltype(ACT_)::value;
-      if (a.z_codes && ACT != ACT_NONE) {
-        if (vec) dz_kernel<DT, ACT, true, true><<<grid, 256, 0, s>>>(a);
-        else dz_kernel<DT, ACT, false, true><<<grid, 256, 0, s>>>(a);
-      } else {
-        if (vec) dz_kernel<DT, ACT, true, false><<<grid, 256, 0, s>>>(a);
-        else dz_kernel<DT, ACT, false, false><<<grid, 256, 0, s>>>(a);
-      }
+      if (vec) dz_kernel<DT, ACT, true><<<grid, 256, 0, s>>>(a);
+      else dz_kernel<DT, ACT, false><<<grid, 256, 0, s>>>(a);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -439,7 +471,19 @@ hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
   d.ld = pad8(a.n);
   d.offsets = a.offsets;
   d.groups = a.groups;
-  hipError_t e = launch_dz<DT>(d, a.act, a.dbias, s);
+  CodeArgs codes{};
+  const bool wide = a.eight && a.dw;
+  if (wide) {
+    codes.codes_in = a.x_codes;
+    codes.scale_in = a.x_scale;
+    codes.out = ws + at.x8;
+    codes.rows = a.m;
+    codes.cols = a.k;
+    codes.ld = pad8(a.k);
+    codes.group = 128;
+    codes.act = a.x_act;
+  }
+  hipError_t e = launch_dz<DT>(d, a.act, a.dbias, wide ? &codes : nullptr, s);
   if (e != hipSuccess || !products) return e;
   const void *x = a.x, *w = a.w, *dz = copy ? d.dz : a.dout;
   if (a.k % 8) {
@@ -449,22 +493,7 @@ hipError_t grad_dt(const LinearGradArgs& a, hipStream_t s) {
     x = ws + at.x8;
     w = ws + at.w8;
   }
-  if (a.eight && a.dw && a.m > 0) {
-    // x's values in 16 bits, which the product reads in many tiles: 4096 x 4096 in 13 us of 390
-    CodeArgs c{};
-    c.codes_in = a.x_codes;
-    c.scale_in = a.x_scale;
-    c.out = ws + at.x8;
-    c.rows = a.m;
-    c.cols = a.k;
-    c.ld = pad8(a.k);
-    c.group = 128;
-    c.dtype = a.dtype;
-    c.act = a.x_act;
-    e = launch_dequant_rows(c, s);
-    if (e != hipSuccess) return e;
-    x = ws + at.x8;
-  }
+  if (wide) x = ws + at.x8;
   Product p{};
   p.offsets = a.offsets;
   p.groups = a.groups;

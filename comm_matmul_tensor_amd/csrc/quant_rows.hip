@@ -12,8 +12,6 @@
 #include <algorithm>
 
 #include "codes.hpp"
-#include "layer8_kernels.hpp"
-#include "linear_act.hpp"
 
 namespace mc2 {
 namespace {
@@ -75,17 +73,7 @@ __device__ __forceinline__ void store_codes(int8_t* row, int64_t c, int64_t cols
   }
 }
 
-// Threads of a row of `chunks` chunks: the most, up to 256, that leave no more
-// than an eighth of them idle over the row's turns, `least` at least.
-int row_threads(int64_t chunks, int least) {
-  int best = least;
-  for (int t = least; t <= 256; t *= 2)
-    if ((chunks + t - 1) / t * t - chunks <= chunks / 8) best = t;
-  return best;
-}
-
 // ---------------------------------------------------------------- per 128 columns
-constexpr int kFlight = 4;  // chunks that a thread loads before it uses one
 template <int DT, bool VEC>
 __global__ __launch_bounds__(256) void quant_groups(CodeArgs a, int tpr) {
   const int64_t row = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
@@ -196,41 +184,14 @@ hipError_t quant_launch(const CodeArgs& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- and back
-// out's rows are ld apart (a multiple of 8 and the columns past the last one
-// become 0, or cols).
 template <int DT, int ACT, bool VEC>
 __global__ __launch_bounds__(256) void dequant_kernel(CodeArgs a, int tpr) {
-  const int64_t row = (int64_t)blockIdx.x * (256 / tpr) + threadIdx.x / tpr;
-  if (row >= a.rows) return;
-  const int8_t* codes = a.codes_in + row * a.cols;
-  const float* scales = a.scale_in + row * scales_of(a.cols, a.group);
-  uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.ld;
-  for (int64_t c0 = 8 * (int64_t)(threadIdx.x % tpr); c0 < a.ld; c0 += kFlight * 8 * tpr) {
-    u32x2 v[kFlight];
-    float scale[kFlight];
-#pragma unroll
-    for (int u = 0; u < kFlight; u++) {
-      const int64_t c = c0 + u * 8 * tpr, in = c < a.cols ? c : VEC ? a.cols - 8 : 0;
-      v[u] = load_codes<VEC>(codes, VEC ? in : c, a.cols);
-      scale[u] = scales[scale_at(in, a.group)];
-    }
-#pragma unroll
-    for (int u = 0; u < kFlight; u++) {
-      const int64_t c = c0 + u * 8 * tpr;
-      if (c >= a.ld) continue;
-      float f[8];
-      code_values(v[u], scale[u], f);
-#pragma unroll
-      for (int e = 0; e < 8; e++) f[e] = VEC || c + e < a.cols ? act_of<ACT>(f[e]) : 0.0f;
-      store_chunk<VEC, true>(out, c, a.ld, pack8<DT>(f));
-    }
-  }
+  dequant_block<DT, ACT, VEC>(a, tpr, blockIdx.x);
 }
 
 template <int DT, int ACT>
 hipError_t dequant_launch(const CodeArgs& a, hipStream_t s) {
-  const int64_t chunks = (a.cols + 7) / 8;
-  const int tpr = row_threads(chunks, chunks < 8 ? 1 : 8), per = 256 / tpr;
+  const int tpr = dequant_threads(a.cols), per = 256 / tpr;
   const unsigned blocks = (unsigned)((a.rows + per - 1) / per);
   if (a.cols % 8 == 0) dequant_kernel<DT, ACT, true><<<blocks, 256, 0, s>>>(a, tpr);
   else dequant_kernel<DT, ACT, false><<<blocks, 256, 0, s>>>(a, tpr);

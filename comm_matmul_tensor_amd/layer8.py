@@ -9,13 +9,14 @@ are not given are allocated on the stream the kernels run on, and with a
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
 
 from . import _I64, _INT, _P, _TORCH_DT, _check, _lib
 from .layer import (_F32, _FLT, _HALF, _I32, _SZ, _SZP, MC2_ACT_NONE, _half, _like, _linear_sizes, _needed, _on, _place,
-                    _ptr, _tensor, _workspace, _workspace_ok)
+                    _ptr, _tensor, _workspace_ok)
 
 MC2_SCORE_SOFTMAX, MC2_SCORE_SIGMOID = range(2)
 
@@ -36,6 +37,26 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 
 _I8 = torch.int8
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(size_fn: str, m: int, k: int, n: int, groups: int) -> int:
+    """A workspace's size, which depends on these alone (asking the library takes longer than a decoding step's other
+    checks together)."""
+    size = ctypes.c_size_t(0)
+    _check(getattr(_lib, size_fn)(m, k, n, groups, ctypes.byref(size)))
+    return size.value
+
+
+def _space(given, like, size_fn: str, *sizes):
+    """(tensor, pointer, bytes) of a call's workspace; nothing where it needs none."""
+    if given is not None:
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    size = _bytes(size_fn, *sizes)
+    if size == 0:
+        return None, None, 0
+    t = like.new_empty((size,), dtype=torch.uint8)
+    return t, t.data_ptr(), size
 _LOGITS = (torch.float32,) + _HALF
 
 
@@ -215,7 +236,7 @@ def mc2_linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_sca
     _workspace_ok(workspace)
     handle = _place("x x_scale w w_scale bias residual group_offsets out workspace", x, x_scale, w, w_scale, bias,
                     residual, group_offsets, out, workspace)
-    _ws, ws, ws_bytes = _workspace(workspace, x, _lib.mc2_linear_i8_workspace_size, m, k, n, groups)
+    _ws, ws, ws_bytes = _space(workspace, x, "mc2_linear_i8_workspace_size", m, k, n, groups)
     if out is None:
         out = x.new_empty((m, n), dtype=dtype)
     _check(_lib.mc2_linear_i8(x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), _ptr(bias),
@@ -269,7 +290,7 @@ def mc2_linear_act_grad_i8(dout: torch.Tensor, x: torch.Tensor, x_scale: torch.T
     _workspace_ok(workspace)
     handle = _place("dout x x_scale w z z_scale group_offsets dx dw dbias workspace", dout, x, x_scale, w, z, z_scale,
                     group_offsets, dx, dw, dbias, workspace)
-    _ws, ws, ws_bytes = _workspace(workspace, x, _lib.mc2_linear_act_grad_i8_workspace_size, m, k, n, groups)
+    _ws, ws, ws_bytes = _space(workspace, x, "mc2_linear_act_grad_i8_workspace_size", m, k, n, groups)
     if need_dx and dx is None:
         dx = dout.new_empty((m, k))
     if need_dw and dw is None:
