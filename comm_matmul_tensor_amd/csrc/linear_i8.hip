@@ -16,26 +16,21 @@ int64_t pad16(int64_t v) { return (v + 15) / 16 * 16; }
 int64_t pad128(int64_t v) { return (v + 127) / 128 * 128; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Sixteen codes of a row of k from c (a multiple of 16), zeros past its end.
-// VEC: k is a multiple of 16.
+// Sixteen codes of a row of k >= 16 from c (a multiple of 16), the last sixteen
+// where they would pass its end, so that no load waits for a condition; trim16
+// then puts them in place, with zeros past the end.  VEC: k is a multiple of 16.
 template <bool VEC>
 __device__ __forceinline__ u32x4 load16(const int8_t* row, int64_t c, int64_t k) {
-  u32x4 v = {0u, 0u, 0u, 0u};
-  if (c >= k) return v;
-  if (VEC) {
-    v = *reinterpret_cast<const u32x4*>(row + c);
-  } else if (c + 16 <= k) {
-    __builtin_memcpy(&v, row + c, 16);
-  } else if (k >= 16) {  // the row's last sixteen, shifted into place
-    unsigned __int128 t;
-    __builtin_memcpy(&t, row + k - 16, 16);
-    v = __builtin_bit_cast(u32x4, t >> (8 * (int)(c + 16 - k)));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; e++)
-      if (c + e < k) v[e / 4] |= (uint32_t)(uint8_t)row[c + e] << (8 * (e & 3));
-  }
+  const int8_t* p = row + (c + 16 <= k ? c : k - 16);
+  if (VEC) return *reinterpret_cast<const u32x4*>(p);
+  u32x4 v;
+  __builtin_memcpy(&v, p, 16);
   return v;
+}
+__device__ __forceinline__ u32x4 trim16(u32x4 v, int64_t c, int64_t k) {
+  if (c >= k) return u32x4{0u, 0u, 0u, 0u};
+  if (c + 16 <= k) return v;
+  return __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, v) >> (8 * (int)(c + 16 - k)));
 }
 
 // ---------------------------------------------------------------- ragged rows
@@ -57,8 +52,17 @@ __global__ __launch_bounds__(256) void pad_codes(PadArgs a) {
     const int8_t* src = a.src[which] + row * a.k;
     int8_t* dst = a.dst[which] + row * a.ld;
 #pragma unroll 4
-    for (int64_t c = 16 * (int64_t)(threadIdx.x % a.tpr); c < a.ld; c += 16 * a.tpr)
-      *reinterpret_cast<u32x4*>(dst + c) = load16<false>(src, c, a.k);
+    for (int64_t c = 16 * (int64_t)(threadIdx.x % a.tpr); c < a.ld; c += 16 * a.tpr) {
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (a.k >= 16) {
+        v = trim16(load16<false>(src, c, a.k), c, a.k);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+          if (c + e < a.k) v[e / 4] |= (uint32_t)(uint8_t)src[c + e] << (8 * (e & 3));
+      }
+      *reinterpret_cast<u32x4*>(dst + c) = v;
+    }
   }
 }
 
@@ -92,6 +96,15 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_i8_kernel(Product p, int64_
       fw[u] = load16<VEC>(w, c, k);
 #pragma unroll
       for (int i = 0; i < MF; i++) fx[i][u] = load16<VEC>(x[i], c, k);
+    }
+    if (kb + 64 * kSkinnyU > k) {
+#pragma unroll
+      for (int u = 0; u < kSkinnyU; u++) {
+        const int64_t c = kb + 64 * u + 16 * (lane / 16);
+        fw[u] = trim16(fw[u], c, k);
+#pragma unroll
+        for (int i = 0; i < MF; i++) fx[i][u] = trim16(fx[i][u], c, k);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kSkinnyU; u++)
@@ -139,7 +152,7 @@ int skinny_waves(int64_t m, int64_t k, int64_t n) {
 // rows 32.2, 31.2; 1 row 33.3, 28.1).  16 rows of 4096 x 4096 7.5, tiles 10.1; of 4096 x
 // 7168 10.9, 10.3; 24 rows of 1792 x 7168 8.2, 7.6.
 bool skinny(int64_t m, int64_t k, int64_t n, int64_t groups, const Plan& tiles) {
-  if (groups || m > kSkinnyRows) return false;
+  if (groups || m > kSkinnyRows || k < 16) return false;  // (its loads are of 16 codes)
   if (m <= 8) return true;
   const double bytes = (double)n * (double)k, cus = std::max(1.0, (double)n / 16.0 / 256.0);
   const double here = std::max((double)(16 + m) * (double)k * cus / 30e3, bytes / 5e6);
@@ -171,7 +184,7 @@ struct LayoutI8 {
       total += up256(bytes);
       return at;
     };
-    if (groups || m > 8) plan = plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups, true);
+    if (groups || m > 8 || k < 16) plan = plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups, true);
     few = skinny(m, k, n, groups, plan);
     if (few) plan = Plan{};
     const bool ragged = k % 16 != 0 && !few;
