@@ -242,6 +242,7 @@ struct DzArgs {
   int tpr;
   const int8_t* z_codes;  // EIGHT: z as codes, a scale per 128 columns
   const float* z_scale;
+  uint16_t* dbias;  // EIGHT, one tile of rows: its sums are the bias's gradient (else NULL)
 };
 // Tile (bx, by) of it; red: 256 * 8 numbers, [row of threads][column].
 template <int DT, int ACT, bool VEC, bool EIGHT>
@@ -279,14 +280,15 @@ __device__ __forceinline__ void dz_tile(const DzArgs& a, unsigned bx, unsigned b
       if (a.dz) *reinterpret_cast<u32x4*>(a.dz + row * a.ld + c) = pack8<DT>(d);
     }
   }
-  if (!a.partial) return;
+  if (!a.partial && !(EIGHT && a.dbias)) return;
 #pragma unroll
   for (int e = 0; e < 8; e++) red[rt * (8 * tpr) + 8 * ct + e] = sum[e];
   __syncthreads();
   for (int i = threadIdx.x; i < 8 * tpr && c0 + i < a.n; i += 256) {
     float s = red[i];
     for (int r = 1; r < rows; r++) s += red[r * (8 * tpr) + i];
-    a.partial[(int64_t)bx * a.n + c0 + i] = s;
+    if (EIGHT && a.dbias) a.dbias[c0 + i] = enc16<DT>(s);
+    else a.partial[(int64_t)bx * a.n + c0 + i] = s;
   }
 }
 template <int DT, int ACT, bool VEC>
@@ -346,6 +348,7 @@ hipError_t launch_dz(DzArgs a, int act, void* dbias, const CodeArgs* wide, hipSt
   const bool vec = a.n % 8 == 0;
   const bool sums = a.dz || dbias;
   if (a.m > 0 && (wide || (a.z_codes && sums))) {
+    if (tiles == 1 && dbias) a.dbias = static_cast<uint16_t*>(dbias);
     const unsigned cols = sums ? (unsigned)((a.n + 8 * a.tpr - 1) / (8 * a.tpr)) : 0;
     const CodeArgs x = wide ? *wide : CodeArgs{};
     const int tpr = wide ? dequant_threads(x.cols) : 1;
@@ -370,7 +373,7 @@ hipError_t launch_dz(DzArgs a, int act, void* dbias, const CodeArgs* wide, hipSt
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (dbias) {
+  if (dbias && !a.dbias) {
     const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)std::max<int64_t>(a.groups, 1));
     dbias_kernel<DT><<<grid, 256, 0, s>>>(a, tiles, static_cast<uint16_t*>(dbias));
     return hipGetLastError();
