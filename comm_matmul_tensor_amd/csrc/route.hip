@@ -19,8 +19,9 @@
 // fp32 with an error bound (Doubt).  Where two neighbours of the order lie
 // within it, a tie among them, fp64 decides: on the chosen and the next few
 // alone where that is enough (order64), else on the whole row (choose64), 3
-// us for the rows of a batch that need it.  So the experts chosen are those of
-// fp64, at fp32's cost.
+// us for the few rows of a batch that need it (8191 rows of equal logits: 25).  So
+// the experts chosen are those of fp64, at fp32's cost; bf16 logits under a
+// bias of zeros, which tie in many rows, take 10 us.
 #include "layer8_kernels.hpp"
 #include "layer_device.hpp"
 
@@ -289,16 +290,30 @@ __device__ __forceinline__ bool is_kept(unsigned long long kept, int g) {
   return (g & 32 ? (uint32_t)(kept >> 32) : (uint32_t)kept) >> (g & 31) & 1;
 }
 
-// The chosen of a team in their true order (their set is right): each lane's
-// logit, or sigmoid's c in fp64, and its place among them.  (A softmax's c needs
-// every logit: choose64.)
-template <int TEAM, int DT>
-__device__ __forceinline__ int order64(const RouteArgs& a, int64_t row, int id, int count) {
+template <int TEAM>
+__device__ __forceinline__ uint32_t send(uint32_t v, int to) {  // to lane `to` of the team
   const int lane = threadIdx.x % TEAM;
-  double c = -__builtin_inf();
+  return (uint32_t)__builtin_amdgcn_ds_permute(4 * (int)(threadIdx.x % 64 - lane + to), (int)v);
+}
+// The first count of a team in the order of fp64 (their set is right): each
+// lane's logit, or its c in fp64, and its place among them.  A softmax's p is
+// then that of the fp32 sum, whose error of 2^-17 at most all p share: it moves
+// the difference of two c by that part of the difference of their p.  Returns
+// whether two neighbours are still in doubt.
+template <int TEAM, int DT>
+__device__ __forceinline__ bool order64(const RouteArgs& a, int64_t row, int count, float m, float sum, int& id) {
+  const int lane = threadIdx.x % TEAM;
+  const bool softmax = a.score == SCORE_SOFTMAX;
+  float l = 0.0f, b = 0.0f;
+  double c = -__builtin_inf(), p = 0.0;
   if (id >= 0) {
-    c = (double)logit_at<DT>(a.logits, row + id);
-    if (a.bias) c = 1.0 / (1.0 + exp(-c)) + (double)a.bias[id];
+    l = logit_at<DT>(a.logits, row + id) + 0.0f;
+    c = (double)l;
+    if (a.bias) {
+      b = a.bias[id];
+      p = softmax ? exp(c - (double)m) / (double)sum : 1.0 / (1.0 + exp(-c));
+      c = p + (double)b;
+    }
   }
   int place = 0;
   for (int j = 0; j < count; j++) {
@@ -307,7 +322,18 @@ __device__ __forceinline__ int order64(const RouteArgs& a, int64_t row, int id, 
     place += u > c || (u == c && other < id);
   }
   const int to = id < 0 ? lane : place;  // (those without an expert come last already)
-  return __builtin_amdgcn_ds_permute(4 * (int)(threadIdx.x % 64 - lane + to), id);
+  id = (int)send<TEAM>((uint32_t)id, to);
+  if (!softmax || !a.bias) return false;
+  const u32x2 pb = __builtin_bit_cast(u32x2, p), cb = __builtin_bit_cast(u32x2, c);
+  p = __builtin_bit_cast(double, u32x2{send<TEAM>(pb[0], to), send<TEAM>(pb[1], to)});
+  c = __builtin_bit_cast(double, u32x2{send<TEAM>(cb[0], to), send<TEAM>(cb[1], to)});
+  l = __uint_as_float(send<TEAM>(__float_as_uint(l), to));
+  b = __uint_as_float(send<TEAM>(__float_as_uint(b), to));
+  const int from = lane > 0 ? lane - 1 : 0;
+  const double gap = __shfl(c, from, TEAM) - c, apart = fabs(__shfl(p, from, TEAM) - p);
+  const bool alike = __shfl(l, from, TEAM) == l && __shfl(b, from, TEAM) == b;  // equal c whatever the sum
+  const bool open = lane > 0 && lane < count && id >= 0 && !alike && !(gap > apart * 0x1p-17 + fabs(c) * 0x1p-50);
+  return team_max<TEAM>(open ? 1 : 0) != 0;
 }
 
 // The choice for one token with all scores in fp64, by the whole wavefront;
@@ -466,11 +492,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread 
   open = max(open, a.bias ? pick<TEAM, SLOTS, true>(key, a.top, keys_doubt, false, id, count)
                           : pick<TEAM, SLOTS, false>(key, a.top, keys_doubt, DT != DT_F32, id, count));
   if (wrong) open = SURE;
-  if (!(softmax && a.bias) && __ballot(open == ORDER)) {
-    const int ordered = order64<TEAM, DT>(a, row, id, count);
+  if (__ballot(open == ORDER)) {
+    int ordered = id;
+    const bool still = order64<TEAM, DT>(a, row, count, m, sum, ordered);
     if (open == ORDER) {
       id = ordered;
-      open = SURE;
+      open = still ? CHOICE : SURE;
     }
   }
   for (unsigned long long again = __ballot(open != SURE); again;) {

@@ -64,7 +64,10 @@ def test_sizes(mc2, tokens, experts, top, dtype, score):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_groups(mc2, experts, groups, top_groups, top, group_top, score):
     if group_top > experts // groups:
-        pytest.skip("refused")
+        with pytest.raises(mc2.Mc2Error, match="group_top"):
+            mc2.mc2_moe_route(torch.zeros((1, experts), device="cuda"), top, groups=groups, top_groups=top_groups,
+                              group_top=group_top)
+        return
     print(f"route groups {experts} / {groups} top {top_groups} {top} sum {group_top} {score}", flush=True)
     g = torch.Generator().manual_seed(groups)
     for dtype, biased in (("f32", False), ("f32", True), ("bf16", False), ("f16", True)):
@@ -106,6 +109,18 @@ def test_near_ties_are_those_of_64_bits(mc2):
             l += torch.randn(l.shape, generator=g) * torch.logspace(-9, -3, 40)[:, None]
             run(mc2, l, 8, bias, score)
             run(mc2, l, 6, bias, score, groups=8, top_groups=3, group_top=2)
+
+
+def test_a_bias_of_zeros(mc2):
+    """Ties as 16-bit logits have them, under a bias that says nothing: the order of the logits, then of the experts."""
+    for dtype in ("bf16", "f16", "f32"):
+        l = logits_of(18, 300, 256, dtype, std=1.0)
+        for score in ("softmax", "sigmoid"):
+            ids, _ = run(mc2, l, 8, torch.zeros((256,)), score)
+            plain, _ = run(mc2, l, 8, None, score)
+            assert torch.equal(ids, plain)
+            run(mc2, l, 8, torch.zeros((256,)), score, groups=16, top_groups=5, group_top=2)
+            run(mc2, l, 20, torch.zeros((256,)), score)
 
 
 def test_bias_that_swamps_the_scores(mc2):
