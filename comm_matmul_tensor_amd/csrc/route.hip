@@ -507,11 +507,14 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread 
     if (team == t) id = moved;
     again &= ~(((TEAM < 64 ? 1ull << TEAM : 0ull) - 1) << (t * TEAM));
   }
-  float w = 0.0f;
-  if (there && lane < a.top && id >= 0) {
-    const float v = logit_at<DT>(a.logits, row + id);
-    w = softmax ? exp_near(v - m) : 1.0f / (1.0f + exp_near(-v));
+  const bool chosen = there && lane < a.top && id >= 0;
+  float w = 0.0f, v = ninf;
+  if (chosen) v = logit_at<DT>(a.logits, row + id) + 0.0f;
+  if (softmax && a.renormalise) {  // shares of the chosen alone, however far below the others
+    const uint32_t k = team_max<TEAM>(chosen ? key_of(v) : kOff);
+    m = k == kOff ? 0.0f : of_key(k);
   }
+  if (chosen) w = softmax ? exp_near(v - m) : 1.0f / (1.0f + exp_near(-v));
   if (a.renormalise) sum = team_sum<TEAM>(w);
   if (there && lane < a.top) {
     a.ids[token * a.top + lane] = wrong ? -1 : id;

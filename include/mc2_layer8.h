@@ -41,7 +41,7 @@ typedef enum {
  *     chosen p.
  *   expert_ids  (tokens, top) int32; -1 where fewer than top experts are on
  *   weights     (tokens, top) fp32; 0 there, and 0 for all if renormalise and
- *               the chosen p sum to 0
+ *               the chosen sigmoids are all 0 in fp32
  * A token with a NaN among its logits, or with softmax a logit of +inf, has no
  * experts: ids -1, weights NaN.  (mc2_moe_permute drops an id of -1.)
  * c is compared in fp32 where its error there leaves no doubt about the

@@ -47,7 +47,10 @@ def route(logits, top, bias=None, score="softmax", groups=1, top_groups=1, group
         for j, e in enumerate(order):
             ids[t, j] = e
             w[t, j] = p[t, e]
-    if renorm:
+    if renorm and score == "softmax":  # shares of the chosen alone: their scores may all round to 0
+        v = torch.where(ids >= 0, l.gather(1, ids.long().clamp(min=0)), torch.full_like(w, NINF))
+        w = torch.where(torch.isnan(w), w, torch.nan_to_num(scores(v, score)))
+    elif renorm:
         s = w.sum(1, keepdim=True)
         w = torch.where(s > 0, w / s, torch.where(torch.isnan(s), w, torch.zeros_like(w)))
     return ids, w * scale, p

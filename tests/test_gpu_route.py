@@ -170,6 +170,20 @@ def test_nan_and_infinity(mc2):
             assert torch.isfinite(w).all() and (w >= 0).all() and (w <= 1).all()
 
 
+def test_shares_of_experts_far_below_the_others(mc2):
+    """The kept group's logits are so far below the best one that its scores are 0 in fp32: their shares are not."""
+    l = torch.tensor([[0.0, -1.0, -500.0, -501.0], [3.0, 3.0, -1e4, -1e4]])
+    bias = torch.tensor([0.0, 0.0, 5.0, 5.0])
+    ids, w = run(mc2, l, 2, bias, "softmax", groups=2, top_groups=1, group_top=2)
+    assert torch.equal(ids.cpu(), torch.tensor([[2, 3], [2, 3]], dtype=torch.int32))
+    share = torch.sigmoid(torch.tensor([1.0, -1.0], dtype=torch.float64))
+    check(w[0].cpu(), share, 32 * EPS32 * share, "shares")
+    assert torch.equal(w[1].cpu(), torch.tensor([0.5, 0.5]))
+    got = mc2.mc2_moe_route_grad(torch.tensor([[1.0, 0.0], [1.0, 0.0]]).cuda(), l.cuda(), ids)
+    want = torch.tensor([float(share[0] * share[1]), 0.25], dtype=torch.float64)
+    check(got[:, 2].cpu(), want, 64 * EPS32 * want, "gradient")
+
+
 def test_no_tokens_outputs_given_and_streams(mc2):
     ids, w = mc2.mc2_moe_route(torch.empty((0, 8), device="cuda"), 2)
     assert ids.shape == (0, 2) and w.shape == (0, 2)
