@@ -15,7 +15,8 @@
 // Operands: A K-contiguous (AK: stored (m, k)) or M-contiguous ((k, m)); B
 // K-contiguous (BK: (n, k)) or N-contiguous ((k, n)).  Their leading
 // dimensions are multiples of 8 elements (the launcher copies others), so
-// every 16-byte chunk of a row is aligned; m, n and k are arbitrary.
+// every 16-byte chunk of a row is aligned; m, n and k are arbitrary.  With I8
+// they may be multiples of 4 bytes: buffer loads of 16 bytes need no more.
 //
 // Tile.  A workgroup of WGM x WGN wavefronts makes a BM x BN tile of C in
 // 16 x 16 MFMA tiles, 64 of K at a time.  Both operands go from memory to LDS
@@ -68,7 +69,7 @@ constexpr int kMaxDim = 1 << 21;  // n and k: 256 rows of an operand stay below 
 
 struct Product {
   const void *a, *b;
-  int64_t lda, ldb;                 // elements between rows as stored, multiples of 8
+  int64_t lda, ldb;                 // elements between rows as stored, multiples of 8 (I8: of 2)
   int64_t m, n, k;
   // groups (0: none).  BY_ROWS: ranges of C's rows, B and bias of group g at
   // g b_group, g n; BY_K: ranges of the contraction (rows of A and B as
@@ -85,6 +86,7 @@ struct Product {
   float* partial;
   int tile_group, order_cols;       // order of the tiles (tile_at)
   const float *a_scale, *b_scale;   // I8: of A's rows, of C's columns (group g's at g n)
+  int tail;                         // I8: codes of a row past the k pairs: 0, 4, 8 or 12
 };
 
 enum : int { DENSE = 0, BY_ROWS = 1, BY_K = 2 };
@@ -550,6 +552,36 @@ __global__ __launch_bounds__(64 * WGM * WGN) void product_kernel(Product p) {
     wait_vmcnt<0>();  // the last loads' zeros are in LDS before the epilogue's values
   }
 
+  if constexpr (I8) {
+    // The last codes of rows that are no multiple of 16: the whole chunks went
+    // through LDS, and what is left is one more MFMA of each 16 x 16 tile, its
+    // operands straight from memory (the last part's, with K in parts).
+    if (p.tail && scaled && (GMODE != DENSE || p.splits < 2 || (int)blockIdx.y == p.splits - 1)) {
+      auto last = [&](const uint16_t* rows, int64_t ld, int64_t row) {
+        const uint32_t* at = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(rows) + row * ld * 2 +
+                                                               p.k * 2);
+        u32x4 v = {at[0], 0u, 0u, 0u};
+        if (p.tail > 4) v[1] = at[1];
+        if (p.tail > 8) v[2] = at[2];
+        return lane < 16 ? v : u32x4{0u, 0u, 0u, 0u};
+      };
+      u32x4 ta[FM], tb[FN];
+#pragma unroll
+      for (int i = 0; i < FM; i++) {
+        const int64_t row = m0 + wm * WM + 16 * i + lane % 16;
+        ta[i] = last(a, p.lda, row < m_end ? row : m_end - 1);
+      }
+#pragma unroll
+      for (int j = 0; j < FN; j++) {
+        const int64_t col = n0 + wn * WN + 16 * j + lane % 16;
+        tb[j] = last(b, p.ldb, col < p.n ? col : p.n - 1);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; i++)
+#pragma unroll
+        for (int j = 0; j < FN; j++) acc[i][j] = mfma_any<DT, I8>(tb[j], ta[i], acc[i][j]);
+    }
+  }
   if constexpr (GMODE == DENSE && BN < 256) {
     if (p.splits > 1) {  // fp32 sums of the rows there are, whole tiles of columns
       const int64_t ld = (int64_t)tiles_n * BN;

@@ -173,11 +173,25 @@ hipError_t launch_skinny(const Product& p, int64_t k, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Whether the tiles read rows copied to whole cache lines.  Rows of a multiple of
+// 4 bytes can be loaded where they stand, in 16-byte chunks that lie across the
+// lines: 64 rows for 32 experts of 4008 x 2040 55.7 us (149.5 with the copy), 517
+// rows of 1000 x 2000 8.5 (11.7), 8191 of 1000 x 1000 20.8 (25.0).  A step's loads
+// then touch twice the lines, which costs a product bound by its MFMAs about a
+// third of their time, and may be more than the copy: 4095 rows of 4008 x 5000
+// 117.6 (100.4 with the copy), of 1000 x 5000 52.8 (50.1).
+bool pads(int64_t m, int64_t k, int64_t n, int64_t groups) {
+  const double matrices = (double)std::max<int64_t>(groups, 1);
+  const double mfma_us = 2.0 * (double)m * (double)n * (double)k / 2.1e9;
+  const double copy_us = 3.0 + 2.0 * ((double)m + matrices * (double)n) * (double)k / 5.3e6;
+  return k % 4 != 0 || (k % 16 != 0 && 0.35 * mfma_us > copy_us);
+}
+
 // Parts of the workspace, each 256-byte aligned.
 struct LayoutI8 {
   size_t x, w, partial, total = 0;
   Plan plan{};
-  bool few;  // the product of few rows
+  bool few, padded;  // the product of few rows; tiles of rows copied to an aligned width
   LayoutI8(int64_t m, int64_t k, int64_t n, int64_t groups) {
     auto take = [&](size_t bytes) {
       const size_t at = total;
@@ -187,9 +201,9 @@ struct LayoutI8 {
     if (groups || m > 8 || k < 16) plan = plan_product(m, n, pad16(k) / 2, 0, groups ? BY_ROWS : DENSE, groups, true);
     few = skinny(m, k, n, groups, plan);
     if (few) plan = Plan{};
-    const bool ragged = k % 16 != 0 && !few;
-    x = take(ragged ? (size_t)m * pad128(k) : 0);
-    w = take(ragged ? (size_t)std::max<int64_t>(groups, 1) * n * pad128(k) : 0);
+    padded = !few && pads(m, k, n, groups);
+    x = take(padded ? (size_t)m * pad128(k) : 0);
+    w = take(padded ? (size_t)std::max<int64_t>(groups, 1) * n * pad128(k) : 0);
     partial = take(plan.partial_bytes);
   }
 };
@@ -205,7 +219,8 @@ hipError_t linear_i8_dt(const LinearI8Args& a, hipStream_t s) {
   p.b_scale = a.w_scale;
   p.m = a.m;
   p.n = a.n;
-  p.k = pad16(a.k) / 2;
+  p.k = (at.padded ? pad16(a.k) : a.k / 16 * 16) / 2;
+  p.tail = at.padded ? 0 : (int)(a.k % 16);
   p.offsets = a.offsets;
   p.groups = a.groups;
   p.bias = a.bias;
@@ -214,9 +229,9 @@ hipError_t linear_i8_dt(const LinearI8Args& a, hipStream_t s) {
   p.act = a.act;
   p.splits = 1;
   if (at.few) return a.m <= 16 ? launch_skinny<DT, 1>(p, a.k, s) : launch_skinny<DT, 2>(p, a.k, s);
-  p.lda = p.ldb = (a.k % 16 ? pad128(a.k) : a.k) / 2;
+  p.lda = p.ldb = (at.padded ? pad128(a.k) : a.k) / 2;
   p.b_group = a.n * p.ldb;
-  if (a.k % 16) {
+  if (at.padded) {
     const int64_t matrices = std::max<int64_t>(a.groups, 1);
     PadArgs pad{{a.x, a.w},
                 {reinterpret_cast<int8_t*>(ws + at.x), reinterpret_cast<int8_t*>(ws + at.w)},

@@ -70,7 +70,7 @@ def run(mc2, seed, m, k, n, dtype, name, bias, residual, offsets=None, full=Fals
 SIZES = [(1, 1, 1), (1, 16, 16), (1, 4096, 1792), (2, 33, 7), (5, 264, 100), (16, 512, 4100), (17, 1000, 65),
          (32, 2049, 33), (33, 64, 64), (33, 63, 65), (64, 4096, 256), (100, 40, 1000), (129, 136, 127), (128, 16, 8),
          (257, 129, 131), (300, 200, 520), (517, 1792, 384), (1, 5, 3000), (256, 1, 256), (700, 72, 1), (1000, 576, 777),
-         (9, 15, 40), (40, 15, 40), (40, 17, 41), (64, 128, 64), (64, 144, 64), (48, 31, 16)]
+         (9, 15, 40), (40, 4, 40), (40, 8, 41), (70, 12, 39), (100, 20, 64), (65, 1016, 100), (40, 15, 40), (40, 17, 41), (64, 128, 64), (64, 144, 64), (48, 31, 16)]
 
 
 @pytest.mark.parametrize("m,k,n", SIZES)
@@ -110,7 +110,7 @@ GROUPS = [
 
 
 @pytest.mark.parametrize("m,offsets", GROUPS)
-@pytest.mark.parametrize("k,n", [(512, 128), (400, 264), (77, 39)])
+@pytest.mark.parametrize("k,n", [(512, 128), (400, 264), (77, 39), (4, 39), (204, 264), (136, 40), (76, 39)])
 def test_groups(mc2, m, offsets, k, n):
     print(f"groups m={m} k={k} n={n} offsets={offsets[:8]}", flush=True)
     run(mc2, 21, m, k, n, "bf16", "silu", True, True, offsets)

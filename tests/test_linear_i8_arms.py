@@ -82,9 +82,31 @@ def test_few_rows_or_tiles():
         assert arm(m, k, n, 0)[1] == f"few rows, {waves}", (m, k, n)
 
 
+# The tiles' cases with rows of a multiple of 4 bytes, not of 16: the last 4, 8 or 12 codes by themselves.
+TAILS = [(m, k // 16 * 16 + 4 + 4 * (i % 3), n, groups, name, parts)
+         for i, (m, k, n, groups, name, parts) in enumerate(CASES) if "rows" not in name]
+
+
+def space(m, k, n, groups):
+    got = ctypes.c_size_t()
+    assert lib.mc2_linear_i8_workspace_size(I(m), I(k), I(n), I(groups), ctypes.byref(got)) == 0
+    return got.value
+
+
+def test_rows_read_where_they_stand():
+    """Copied: rows of no multiple of 4, and of the others those of products that the copy makes faster."""
+    for m, k, n, groups, name, parts in TAILS:
+        assert arm(m, k, n, groups) == (groups > 0, name, parts), (m, k, n, groups)
+    copied = [space(m, k, n, groups) >= (m + max(groups, 1) * n) * k for m, k, n, groups, _, _ in TAILS]
+    assert copied.count(False) >= len(TAILS) - 4
+    for m, k, n, groups, rows in [(4095, 4008, 5000, 0, True), (8191, 1000, 1000, 0, False), (64, 4008, 2040, 32, False),
+                                  (64, 4006, 2040, 32, True), (64, 4096, 2040, 32, False), (517, 1001, 2000, 0, True)]:
+        assert (space(m, k, n, groups) >= (m + max(groups, 1) * n) * k) == rows, (m, k, n, groups)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("case", CASES + TAILS, ids=lambda c: "-".join(map(str, c)))
 def test_results(case, dtype):
     m, k, n, groups = case[:4]
     rnd, lead, G, off, parts = inputs(m, k, n, groups, dtype)
