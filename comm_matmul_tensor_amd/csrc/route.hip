@@ -200,7 +200,11 @@ struct Two {
     b = fmax(fmax(b, d), fmin(a, c));
     a = fmax(a, c);
   }
-  __device__ __forceinline__ T value(int group_top) const { return group_top == 2 && b > -__builtin_inf() ? a + b : a; }
+  // (a sum past fp32's lowest number is that number, a group still; equal ones are in doubt)
+  __device__ __forceinline__ T value(int group_top) const {
+    if (group_top != 2 || !(b > -__builtin_inf())) return a;
+    return sizeof(T) == 4 ? fmax(a + b, (T)-3.402823466e38f) : a + b;
+  }
 };
 
 // The groups of a lane's experts: (e + 0.5) / per in fp32 is off by less than

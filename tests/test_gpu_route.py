@@ -152,6 +152,24 @@ def test_experts_that_are_off(mc2, score):
     assert (ids == -1).all() and torch.count_nonzero(w) == 0
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_at_the_ends_of_the_type(mc2, score):
+    """A group's two scores of the lowest or the largest bias have a sum past fp32: lower or higher than any one of them,
+    and a group still."""
+    low, big = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    for experts, groups, top in ((32, 4, 16), (32, 4, 9), (96, 8, 30), (512, 8, 64)):
+        per = experts // groups
+        l = logits_of(experts + top, 6, experts, "f32")
+        for value in (low, big, -math.inf):
+            bias = torch.full((experts,), value)
+            bias[per:2 * per] = 0.0                      # one group at its scores
+            run(mc2, l, top, bias, score, groups=groups, top_groups=max(2, -(-top // per)), group_top=2)
+            bias[3 * per:4 * per - 1] = -math.inf        # one with a single expert: its value is not a sum
+            run(mc2, l, top, bias, score, groups=groups, top_groups=max(2, -(-top // per)), group_top=2)
+            bias[2 * per] = 0.75 * value                 # sums that differ past fp32's range
+            run(mc2, l, top, bias, score, groups=groups, top_groups=max(2, -(-top // per)), group_top=2)
+
+
 def test_nan_and_infinity(mc2):
     l = logits_of(8, 6, 33, "f32")
     l[1, 32] = math.nan
