@@ -47,9 +47,13 @@ inline int row_threads(int64_t chunks, int least) {
     if ((chunks + t - 1) / t * t - chunks <= chunks / 8) best = t;
   return best;
 }
-inline int dequant_threads(int64_t cols) {
+// (A launch has fewer than 2^32 threads: at most 2^22 workgroups here, as the
+// gradient's launch has others beside them.)
+inline int dequant_threads(int64_t rows, int64_t cols) {
   const int64_t chunks = (cols + 7) / 8;
-  return row_threads(chunks, chunks < 8 ? 1 : 8);
+  int threads = row_threads(chunks, chunks < 8 ? 1 : 8);
+  while (threads > 1 && rows > (int64_t)(256 / threads) << 22) threads /= 2;
+  return threads;
 }
 
 constexpr int kFlight = 4;  // chunks that a thread loads before it uses one

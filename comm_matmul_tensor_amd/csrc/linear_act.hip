@@ -351,7 +351,7 @@ hipError_t launch_dz(DzArgs a, int act, void* dbias, const CodeArgs* wide, hipSt
     if (tiles == 1 && dbias) a.dbias = static_cast<uint16_t*>(dbias);
     const unsigned cols = sums ? (unsigned)((a.n + 8 * a.tpr - 1) / (8 * a.tpr)) : 0;
     const CodeArgs x = wide ? *wide : CodeArgs{};
-    const int tpr = wide ? dequant_threads(x.cols) : 1;
+    const int tpr = wide ? dequant_threads(x.rows, x.cols) : 1;
     const unsigned blocks = (unsigned)tiles * cols + (wide ? (unsigned)((x.rows + 256 / tpr - 1) / (256 / tpr)) : 0);
     auto kept = [&](auto VECN_, auto VECK_) {
       kept_kernel<DT, decltype(VECN_)::value, decltype(VECK_)::value>

@@ -159,8 +159,19 @@ __global__ __launch_bounds__(kWide) void quant_wide(CodeArgs a) {
   }
 }
 
+constexpr int64_t kRows = 1 << 21;  // a launch's, so that it has fewer than 2^32 threads
+
 template <int DT, bool VEC>
-hipError_t quant_launch(const CodeArgs& a, hipStream_t s) {
+hipError_t quant_launch(const CodeArgs& given, hipStream_t s) {
+  CodeArgs a = given;
+  for (; a.rows > kRows; a.rows -= kRows) {
+    CodeArgs first = a;
+    first.rows = kRows;
+    if (const hipError_t e = quant_launch<DT, VEC>(first, s); e != hipSuccess) return e;
+    a.x = static_cast<const uint16_t*>(a.x) + kRows * a.cols;
+    a.codes += kRows * a.cols;
+    a.scale += kRows * scales_of(a.cols, a.group);
+  }
   if (a.group) {
     const int tpr = row_threads((a.cols + 127) / 128 * 16, 16), per = 256 / tpr;
     quant_groups<DT, VEC><<<(unsigned)((a.rows + per - 1) / per), 256, 0, s>>>(a, tpr);
@@ -191,7 +202,7 @@ __global__ __launch_bounds__(256) void dequant_kernel(CodeArgs a, int tpr) {
 
 template <int DT, int ACT>
 hipError_t dequant_launch(const CodeArgs& a, hipStream_t s) {
-  const int tpr = dequant_threads(a.cols), per = 256 / tpr;
+  const int tpr = dequant_threads(a.rows, a.cols), per = 256 / tpr;
   const unsigned blocks = (unsigned)((a.rows + per - 1) / per);
   if (a.cols % 8 == 0) dequant_kernel<DT, ACT, true><<<blocks, 256, 0, s>>>(a, tpr);
   else dequant_kernel<DT, ACT, false><<<blocks, 256, 0, s>>>(a, tpr);

@@ -37,6 +37,7 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 
 _I8 = torch.int8
+_LOGITS = (torch.float32,) + _HALF
 
 
 @functools.lru_cache(maxsize=4096)
@@ -57,7 +58,6 @@ def _space(given, like, size_fn: str, *sizes):
         return None, None, 0
     t = like.new_empty((size,), dtype=torch.uint8)
     return t, t.data_ptr(), size
-_LOGITS = (torch.float32,) + _HALF
 
 
 def _codes(t, name: str):
