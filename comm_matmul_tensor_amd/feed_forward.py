@@ -7,7 +7,9 @@ stream, so that blocks chain with the norm's own addition, and train through
 the autograd functions here, whose every step is a libmc2 call: the only torch
 operations are views and, without a `score`, the router's choice (a top-k and a
 softmax).  Their gradients cannot be differentiated again: a second backward
-through them raises.
+through them raises.  A step is captured into a graph forward and backward
+together, while no eager autograd graph of the same parameters lives (its nodes
+stay on the stream they were made on, which a capture may not touch).
 
 With `keep8` a block keeps its linears' input and pre-activation for the
 backward as int8 codes with a scale per 128 columns, and no activation: per

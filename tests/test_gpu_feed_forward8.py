@@ -235,6 +235,43 @@ def test_a_decoding_step_in_a_graph(ff):
         assert torch.equal(out, dense(*moe(x)))
 
 
+@pytest.mark.parametrize("score", [0, 1])
+def test_a_training_step_in_a_graph(ff, score):
+    """Forward and backward of a routed and a dense block that keep 8 bits, captured together while no eager graph of
+    their parameters lives, replayed on new rows and gradients with eager steps between."""
+    torch.manual_seed(8)
+    moe = ff.ExpertsFeedForward(256, 128, experts=8, top=2, keep8=True, score=score, groups=4, top_groups=2, group_top=2,
+                                renormalise=score == 1, balance=True)
+    dense = ff.FeedForward(256, 384, keep8=True)
+    leaves = [*moe.parameters(), *dense.parameters()]
+    x = torch.randn((37, 256), device="cuda").bfloat16().requires_grad_()
+    dout = torch.randn((37, 256), device="cuda").bfloat16()
+
+    def step():
+        out = dense(*moe(x))
+        return out.detach(), *torch.autograd.grad(out, [x, *leaves], dout)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (9, 10, 11):
+        torch.manual_seed(seed)
+        with torch.no_grad():
+            x.copy_(torch.randn((37, 256), device="cuda"))
+            dout.copy_(torch.randn((37, 256), device="cuda"))
+            moe.bias.copy_(torch.randn((8,), device="cuda") * 0.1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
 def test_state_moves_with_the_module(ff):
     torch.manual_seed(7)
     a = ff.Int8ExpertsFeedForward(ff.ExpertsFeedForward(128, 64, experts=4, top=2, score=0, balance=True))
