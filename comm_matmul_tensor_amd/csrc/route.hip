@@ -35,13 +35,33 @@ constexpr uint32_t kOff = 0;                    // key of an expert that is off;
 
 // exp(x) within 2^-22: the argument in base 2 to twice fp32's precision (x log2(e)
 // rounded alone is off by |x| 2^-24).  Past +-200 it is 0 or infinite in fp32.
+// The instruction gives no subnormal numbers: below 2^-126 e is 0, or with LOW
+// formed at 2^64 times its size and scaled down (t + 64 is exact).
+template <bool LOW = false>
 __device__ __forceinline__ float exp_near(float x) {
   x = __builtin_amdgcn_fmed3f(x, -200.0f, 200.0f);
   const float t = x * kLog2eHi;
   const float lo = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return e < __builtin_inff() ? __builtin_fmaf(e * kLn2, lo, e) : e;
+  const bool low = LOW && t < -125.0f;
+  float e = __builtin_amdgcn_exp2f(low ? t + 64.0f : t);
+  e = e < __builtin_inff() ? __builtin_fmaf(e * kLn2, lo, e) : e;
+  return low ? e * 0x1p-64f : e;
 }
+
+// sigmoid(v) = 1 / (1 + exp(-v)) from the exponential of the sign that keeps it
+// exact: for v < 0 exp(v) / (1 + exp(v)).  `base`, 0 or less, scales it by
+// exp(-base): the largest of a token's chosen logits where all of them lie below
+// 0, so that their shares of each other are those of numbers of ordinary size,
+// whatever is left of the sigmoids themselves in fp32 (for v > 0 base is 0).
+// rest: 1 - sigmoid(v), not scaled.
+struct Sigmoid {
+  float p, rest;
+  static __device__ __forceinline__ Sigmoid of(float v, float base) {
+    const float e = exp_near(-__builtin_fabsf(v)), big = 1.0f / (1.0f + e);
+    return v < 0.0f ? Sigmoid{exp_near<true>(v - base) * big, big} : Sigmoid{big, e * big};
+  }
+};
+constexpr float kNoSigmoid = -709.7827f;  // below it 1 / (1 + exp(-v)) is 0 in fp64 too, and so is the share
 
 template <int DT>
 __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
@@ -514,11 +534,12 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread 
   const bool chosen = there && lane < a.top && id >= 0;
   float w = 0.0f, v = ninf;
   if (chosen) v = logit_at<DT>(a.logits, row + id) + 0.0f;
-  if (softmax && a.renormalise) {  // shares of the chosen alone, however far below the others
+  if (a.renormalise) {  // shares of the chosen alone, however far below the others or below 0
     const uint32_t k = team_max<TEAM>(chosen ? key_of(v) : kOff);
     m = k == kOff ? 0.0f : of_key(k);
+    if (!softmax) m = fminf(m, 0.0f);
   }
-  if (chosen) w = softmax ? exp_near(v - m) : 1.0f / (1.0f + exp_near(-v));
+  if (chosen) w = softmax ? exp_near<true>(v - m) : v < kNoSigmoid ? 0.0f : Sigmoid::of(v, m).p;
   if (a.renormalise) sum = team_sum<TEAM>(w);
   if (there && lane < a.top) {
     a.ids[token * a.top + lane] = wrong ? -1 : id;
@@ -576,14 +597,18 @@ __global__ __launch_bounds__(64 * kWaves) void route_grad_kernel(RouteArgs a) {
       const float sum = wave_sum(e), share = sum > 0.0f ? e / sum : 0.0f;
       term = share * (g - wave_sum(share * g));
     } else {
-      // p and 1 - p, each from the exponential of the sign that keeps it exact
-      const float e = exp_near(-__builtin_fabsf(v)), big = 1.0f / (1.0f + e), small = e * big;
-      const float p = id < 0 ? 0.0f : v < 0.0f ? small : big, q = v < 0.0f ? big : small;
+      float m = 0.0f;
+      if (a.renormalise) {
+        const uint32_t k = team_max<64>(id >= 0 && v > -__builtin_inff() ? key_of(v + 0.0f) : kOff);
+        if (k != kOff) m = fminf(of_key(k), 0.0f);
+      }
+      const Sigmoid s = Sigmoid::of(v, m);
+      const float p = id < 0 || v < kNoSigmoid ? 0.0f : s.p;
       if (a.renormalise) {
         const float sum = wave_sum(p), share = sum > 0.0f ? p / sum : 0.0f;
-        term = share * q * (g - wave_sum(share * g));
+        term = share * s.rest * (g - wave_sum(share * g));
       } else {
-        term = p * q * g;
+        term = p * s.rest * g;
       }
     }
     for (int j = 0; j < a.top; j++) {

@@ -40,8 +40,9 @@ typedef enum {
  *   - weights = scale p of the chosen, with renormalise scale p / sum of the
  *     chosen p.
  *   expert_ids  (tokens, top) int32; -1 where fewer than top experts are on
- *   weights     (tokens, top) fp32; 0 there, and 0 for all if renormalise and
- *               the chosen sigmoids are all 0 in fp32
+ *   weights     (tokens, top) fp32; 0 there, and 0 for a sigmoid that is 0 in
+ *               fp64 (logits below -709.78; of the scores that fp32 alone would
+ *               round to 0 renormalise gives the shares that they have)
  * A token with a NaN among its logits, or with softmax a logit of +inf, has no
  * experts: ids -1, weights NaN.  (mc2_moe_permute drops an id of -1.)
  * c is compared in fp32 where its error there leaves no doubt about the

@@ -311,3 +311,32 @@ def test_graph_replay(mc2):
         torch.cuda.synchronize()
         for a, b in zip(out, both()):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ the ends of the scores
+FAR = [[-88.0, -89.0, -200.0, -300.0], [-95.0, -96.0, -97.0, -500.0], [-103.0, -104.0, -110.0, -105.5],
+       [-300.0, -310.0, -400.0, -1e30], [-740.0, -700.5, -710.0, -720.0], [0.5, -88.5, -120.0, -130.0],
+       [-20.0, -90.0, -95.0, -1e4], [-800.0, -801.0, -1e30, -math.inf], [-1e30, -2e30, -3e38, -math.inf]]
+
+
+@pytest.mark.parametrize("scale", [1.0, -1.5])
+def test_sigmoids_far_below_one(mc2, scale):
+    """Logits whose sigmoids are subnormal or 0 in fp32: their shares are those of 64 bits, and so are the shares'
+    gradients; the scores themselves are right down to fp32's last subnormal numbers.
+
+    A share is a quotient of exp(d) / (1 + exp(l)), d a difference to the largest of the chosen (or 0), rounded: |d|
+    half steps; an exponential is within 4, the other factor 6, the product 1, the sum 2, for a share twice that and 2
+    for quotient and scale: 32 + 2 |d|.  A score alone has no sum: 16, and three roundings of half a subnormal step."""
+    l = torch.tensor(FAR)
+    d = torch.tensor([1.0, 1.0, 1.0, 10.0, 9.5, 88.5, 70.0, 0.0, 0.0], dtype=torch.float64)[:, None]
+    for renorm in (True, False):
+        ids, w = mc2.mc2_moe_route(l.cuda(), 2, score=mc2.MC2_SCORE_SIGMOID, renormalise=renorm, scale=scale)
+        want, wr, _ = ref.route(l, 2, None, "sigmoid", renorm=renorm, scale=scale)
+        assert torch.equal(ids.cpu(), want)
+        err = (32 + 2 * d) * EPS32 * wr.abs() if renorm else 16 * EPS32 * wr.abs()
+        check(w, wr, err + 2.0 ** -148, f"weights, renormalise={renorm}")
+        dw = torch.tensor([[1.0, -0.5]]).repeat(len(FAR), 1)
+        got = mc2.mc2_moe_route_grad(dw.cuda(), l.cuda(), ids, score=mc2.MC2_SCORE_SIGMOID, renormalise=renorm,
+                                     scale=scale)
+        grad, size = ref.route_grad(dw, l, want, "sigmoid", renorm, scale)
+        check(got, grad, (96 + 4 * d) * EPS32 * size + 2.0 ** -126, f"gradient, renormalise={renorm}")
