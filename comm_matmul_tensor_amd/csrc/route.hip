@@ -133,7 +133,7 @@ __device__ __forceinline__ double wave_fold(double v, F f) {
 // softmax: its exponential, the sum's additions (SLOTS and 6 in a row) and a
 // product, relative to p, of which 1 / sum is the largest; of a sigmoid:
 // 2^-22 at most.  Twice that for two values, twice more for sums of two; and
-// the additions' own roundings, relative to the values.
+// the additions' own roundings, relative to the values (of sums: Two::slack).
 struct Doubt {
   float abs, rel;
   __device__ __forceinline__ bool operator()(float a, float b) const {  // a >= b: not surely a > b
@@ -220,6 +220,13 @@ struct Two {
     b = fmax(fmax(b, d), fmin(a, c));
     a = fmax(a, c);
   }
+  // What fp32's roundings of the two and of their sum can be at most: relative to
+  // the terms, which may cancel (2^-23 of both, and half of that for the compared
+  // numbers' own).
+  __device__ __forceinline__ T slack(int group_top) const {
+    const T one = (T)0x1p-22 * fabs(a);
+    return group_top != 2 || !(b > -__builtin_inf()) ? one : one + (T)0x1p-22 * fabs(b);
+  }
   // (a sum past fp32's lowest number is that number, a group still; equal ones are in doubt)
   __device__ __forceinline__ T value(int group_top) const {
     if (group_top != 2 || !(b > -__builtin_inf())) return a;
@@ -238,8 +245,8 @@ __device__ __forceinline__ void groups_of(float inv_per, int (&group)[SLOTS]) {
 
 // How groups are spread: 2^shift lanes of the team share one (one where there
 // are more than half as many as lanes); a lane's i-th group is i TEAM / 2^shift
-// past its first.  In LDS a token has its groups' values, `quads` of four, then
-// its scores, a row of per or per + 1 for each group: odd, so that the rows start
+// past its first.  In LDS a token has its groups' values, `quads` of four, their
+// slack, as many, then its scores, a row of per or per + 1 for each group: odd, so that the rows start
 // in different banks (odd_mask: -1 where one is added); then a place that is
 // written only.
 struct Spread {
@@ -252,7 +259,7 @@ __device__ __forceinline__ void lay_out(const RouteArgs& a, const Spread& sp, co
   const int lane = threadIdx.x % TEAM;
 #pragma unroll
   for (int s = 0; s < SLOTS; s++) {
-    const int e = lane + TEAM * s, at = 4 * sp.quads + e + (group[s] & sp.odd_mask);
+    const int e = lane + TEAM * s, at = 8 * sp.quads + e + (group[s] & sp.odd_mask);
     mine[e < a.experts ? at : sp.size - 1] = score(s);
   }
 }
@@ -260,14 +267,15 @@ __device__ __forceinline__ void lay_out(const RouteArgs& a, const Spread& sp, co
 // The groups kept, as a mask (bit g, the same in the team's lanes), from the
 // team's scores at[s] in `mine`, which no other team touches.  For the lane's
 // own groups `least` and `most` become the smallest value kept and the largest
-// dropped.
+// dropped; in fp32 what they may be at least and at most.
 template <int TEAM, typename T>
 __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs& a, const Spread& sp, T* mine, T& least,
                                                           T& most) {
   typedef T T4 __attribute__((ext_vector_type(4)));
   const int wlane = threadIdx.x % 64, lane = wlane % TEAM;
   const T off = -__builtin_inf();
-  const T* scores = mine + 4 * sp.quads;
+  constexpr bool kSlack = sizeof(T) == 4;
+  const T* scores = mine + 8 * sp.quads;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
   const int step = 1 << sp.shift, stride = TEAM >> sp.shift, rows = 4 * sp.quads, pitch = sp.per - sp.odd_mask;
@@ -284,7 +292,10 @@ __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs& a, co
       for (int u = 0; u < 8; u++) t.add(i + u * step < sp.per ? v[u] : off);
     }
     for (int o = 1; o < step; o *= 2) t.join(__shfl_xor(t.a, o), __shfl_xor(t.b, o));
-    if (g < rows && part == 0) mine[g] = g < a.groups ? t.value(a.group_top) : off;
+    if (g < rows && part == 0) {
+      mine[g] = g < a.groups ? t.value(a.group_top) : off;
+      if (kSlack) mine[rows + g] = t.slack(a.group_top);
+    }
   }
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -302,8 +313,9 @@ __device__ __forceinline__ unsigned long long keep_groups(const RouteArgs& a, co
       for (int i = 0; i < 4; i++) rank += o + i < g ? u[i] >= v : u[i] > v;
     }
     const bool is = v > off && rank < a.top_groups;
-    if (is) least = fmin(least, v);
-    else most = fmax(most, v);
+    const T slack = kSlack && g < a.groups ? mine[rows + g] : (T)0;
+    if (is) least = fmin(least, v - slack);
+    else most = fmax(most, v + slack);  // (of a group that is off NaN, which fmax drops)
     unsigned long long bits = __ballot(is);
     if constexpr (TEAM < 64) bits = bits >> (wlane - lane) & ((1ull << TEAM) - 1);
     kept |= bits << g0;
@@ -503,7 +515,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread 
     if (!by_logit) {
       least = -of_key(team_max<TEAM>(key_of(-least)));
       most = of_key(team_max<TEAM>(key_of(most)));
-      if (most != ninf && doubt(least, most)) open = CHOICE;
+      if (most != ninf && !(least - most > doubt.abs)) open = CHOICE;
     }
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) {
@@ -654,7 +666,7 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
   const bool small = a.experts <= 256 && a.top <= 16;
   const int team = small ? 16 : 64, teams = 64 / team;
   Spread sp{per, per % 2 ? 0 : -1, (a.groups + 3) / 4, 0, 0, 1.0f / (float)per};
-  sp.size = (4 * sp.quads + a.groups * (per - sp.odd_mask) + 4) / 4 * 4;
+  sp.size = (8 * sp.quads + a.groups * (per - sp.odd_mask) + 4) / 4 * 4;
   while ((2 << sp.shift) * a.groups <= team) sp.shift++;
   int waves = kWaves;
   size_t lds = 0;

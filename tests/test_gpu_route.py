@@ -340,3 +340,19 @@ def test_sigmoids_far_below_one(mc2, scale):
                                      scale=scale)
         grad, size = ref.route_grad(dw, l, want, "sigmoid", renorm, scale)
         check(got, grad, (96 + 4 * d) * EPS32 * size + 2.0 ** -126, f"gradient, renormalise={renorm}")
+
+
+def test_groups_whose_scores_cancel(mc2):
+    """A group's two values of opposite signs: their sum is small, and its error that of the large values."""
+    p = torch.tensor([0.54, 0.50, 0.53, 0.52])
+    big = torch.tensor([1e6, -1e6, 1e6, -1e6])
+    ids, _ = run(mc2, torch.log(p / (1 - p))[None], 2, big, "sigmoid", groups=2, top_groups=1, group_top=2)
+    assert ids.tolist() == [[2, 3]]
+    for score in ("sigmoid", "softmax"):
+        for seed, size in enumerate((128.0, 1000.0, 3e4, 1e6)):
+            # 16 and 64 lanes a token; 2 experts a group, or 4 of which two hold the large values
+            for experts, groups in ((128, 64), (256, 64), (384, 64)):
+                l = logits_of(seed + experts, 120, experts, "f32")
+                bias = torch.zeros((groups, experts // groups))
+                bias[:, 0], bias[:, 1:] = size, -size
+                run(mc2, l, 6, bias.flatten(), score, groups=groups, top_groups=5, group_top=2)
