@@ -372,6 +372,12 @@ __device__ __forceinline__ bool order64(const RouteArgs& a, int64_t row, int cou
   return team_max<TEAM>(open ? 1 : 0) != 0;
 }
 
+// Whether the choice goes by the logits alone: without a bias, and with one score
+// of each group the groups' order is that of the logits too.
+__device__ __forceinline__ bool goes_by_logit(const RouteArgs& a) {
+  return !a.bias && (a.groups == 1 || a.group_top == 1);
+}
+
 // The choice for one token with all scores in fp64, by the whole wavefront;
 // `mine` has room for a token's scores.
 template <int DT, int SLOTS>
@@ -386,6 +392,7 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, int64_t row, const S
   for (int s = 0; s < SLOTS; s++) l[s] = logit_at<DT>(a.logits, row + min(lane + 64 * s, a.experts - 1));
 #pragma unroll
   for (int s = 0; s < SLOTS; s++) l[s] = lane + 64 * s < a.experts ? l[s] : -__builtin_inff();
+  const bool by_logit = goes_by_logit(a);
   if (softmax) {
 #pragma unroll
     for (int s = 0; s < SLOTS; s++) m = fmax(m, (double)l[s]);
@@ -399,7 +406,8 @@ __device__ __forceinline__ int choose64(const RouteArgs& a, int64_t row, const S
   if (softmax) sum = wave_fold(part, [](double x, double y) { return x + y; });
 #pragma unroll
   for (int s = 0; s < SLOTS; s++) {
-    const double v = (softmax ? c[s] / sum : 1.0 / (1.0 + c[s])) +
+    const double v = by_logit ? (double)l[s] :
+                     (softmax ? c[s] / sum : 1.0 / (1.0 + c[s])) +
                      (a.bias ? (double)a.bias[min(lane + 64 * s, a.experts - 1)] : 0.0);
     c[s] = l[s] > -__builtin_inff() && v > off ? v : off;  // (a NaN is off)
   }
@@ -473,8 +481,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread 
     top_key = max(top_key, l[s] > ninf ? key_of(l[s]) : kOff);
   }
   wrong = team_max<TEAM>(wrong ? 1 : 0) != 0;
-  // with one score of each group the groups' order is that of the logits too
-  const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
+  const bool by_logit = goes_by_logit(a);
   float m = 0.0f, sum = 1.0f;  // softmax: the largest logit, the sum of exp(l - m)
   if (softmax) m = of_key(team_max<TEAM>(top_key));
   uint32_t key[SLOTS];

@@ -72,10 +72,11 @@ def mc2_moe_route(logits: torch.Tensor, top: int, bias: Optional[torch.Tensor] =
                   weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(expert_ids (tokens, top) int32, weights (tokens, top) fp32) of logits (tokens, experts), fp32 or 16-bit.
 
-    The `top` experts of the largest score + bias, in descending order (equal ones: the lowest first); the weights
-    are their scores (without the bias) times scale, with renormalise over their sum.  groups > 1: only experts of
-    the top_groups groups of neighbours whose group_top (1 or 2) largest sum to most.  A logit of -inf turns an
-    expert off; an id is -1 (weight 0) where too few are on, and all are (weights NaN) for a token with a NaN.
+    The `top` experts of the largest score + bias, in descending order (equal ones: the lowest first; without a bias by
+    their logits, also where the scores round to equal numbers); the weights are their scores (without the bias)
+    times scale, with renormalise over their sum.  groups > 1: only experts of the top_groups groups of neighbours
+    whose group_top (1 or 2) largest sum to most.  A logit of -inf turns an expert off; an id is -1 (weight 0) where
+    too few are on, and all are (weights NaN) for a token with a NaN.
     """
     if stream is not None:
         return _on(stream, mc2_moe_route, logits, top, bias, score=score, groups=groups, top_groups=top_groups,

@@ -36,7 +36,10 @@ typedef enum {
  *     are on; the top_groups groups of the largest values are kept (equal
  *     values: the first), the experts of the others are off for this token;
  *   - the `top` largest c that are on are chosen, in descending order (equal
- *     c: the lowest expert first);
+ *     c: the lowest expert first).  Without a bias c rises with l, and the
+ *     order is that of the logits (equal logits: the lowest expert first) also
+ *     where their scores round to equal numbers, as sigmoids of 40 and 41 do
+ *     in fp64; so is the order of groups with group_top 1;
  *   - weights = scale p of the chosen, with renormalise scale p / sum of the
  *     chosen p.
  *   expert_ids  (tokens, top) int32; -1 where fewer than top experts are on
@@ -45,8 +48,8 @@ typedef enum {
  *               round to 0 renormalise gives the shares that they have)
  * A token with a NaN among its logits, or with softmax a logit of +inf, has no
  * experts: ids -1, weights NaN.  (mc2_moe_permute drops an id of -1.)
- * c is compared in fp32 where its error there leaves no doubt about the
- * order, else in fp64: the choice is that of fp64.
+ * Else c is compared in fp32 where its error there leaves no doubt about the
+ * order, and in fp64 otherwise: the choice is that of fp64.
  *
  * logits      (tokens, experts) of dtype: MC2_F32, MC2_F16 or MC2_BF16
  * bias        (experts) fp32 or NULL (0)

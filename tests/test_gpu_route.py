@@ -356,3 +356,27 @@ def test_groups_whose_scores_cancel(mc2):
                 bias = torch.zeros((groups, experts // groups))
                 bias[:, 0], bias[:, 1:] = size, -size
                 run(mc2, l, 6, bias.flatten(), score, groups=groups, top_groups=5, group_top=2)
+
+
+def test_saturated_sigmoids_without_a_bias(mc2):
+    """Logits whose sigmoids are equal even in 64 bits: without a bias the order is the logits' own, with one (of zeros)
+    the scores tie and the lowest expert comes first."""
+    l = torch.tensor([[40.0, 41.0, 39.0, 45.0], [-1000.0, -999.0, -2000.0, -998.0]])
+    ids, _ = run(mc2, l, 2, None, "sigmoid")
+    assert ids.tolist() == [[3, 1], [3, 1]]
+    ids, _ = run(mc2, l, 2, torch.zeros((4,)), "sigmoid")
+    assert ids.tolist() == [[0, 1], [0, 1]]
+    # groups by their best logit go the same way, also for a token whose many equal logits are settled in 64 bits
+    for score in ("sigmoid", "softmax"):
+        l = torch.linspace(1.0, 2.0, 32).repeat(2, 1)
+        l[:, 0], l[:, 16] = 40.0, 41.0
+        l[1, 17:] = 1.0
+        if score == "softmax":
+            l[:, 1:16] -= 900.0
+            l[:, 0], l[:, 16:] = -800.0, l[:, 16:] - 840.0  # both groups' scores are 0 in 64 bits beside the third's
+            l = torch.cat([l, torch.zeros((2, 16))], dim=1)
+        kind = [mc2.MC2_SCORE_SOFTMAX, mc2.MC2_SCORE_SIGMOID][score == "sigmoid"]
+        ids, _ = mc2.mc2_moe_route(l.cuda(), 19 if score == "softmax" else 3, score=kind, groups=l.shape[1] // 16,
+                                   top_groups=l.shape[1] // 16 - 1, group_top=1)
+        first = list(range(32, 48)) if score == "softmax" else []
+        assert ids[0].tolist() == first + [16, 31, 30] and ids[1].tolist() == first + [16, 17, 18], score
