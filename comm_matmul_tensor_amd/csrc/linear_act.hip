@@ -270,7 +270,11 @@ __device__ __forceinline__ void dz_tile(const DzArgs& a, unsigned bx, unsigned b
         else
           unpack8<DT>(load_chunk<VEC>(a.z + row * a.n, c, a.n), f);
 #pragma unroll
-        for (int e = 0; e < 8; e++) d[e] *= act_slope<ACT>(f[e]);
+        for (int e = 0; e < 8; e++) {
+          // (codes of a group that is NaN: relu's slope of a NaN is 0, which would hide 128 columns)
+          const bool lost = EIGHT && ACT == ACT_RELU && f[e] != f[e];
+          d[e] *= lost ? f[e] : act_slope<ACT>(f[e]);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 8; e++) {

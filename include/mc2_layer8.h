@@ -125,7 +125,8 @@ mc2_status mc2_linear_i8(const int8_t* x, const float* x_scale, const int8_t* w,
  * 128).  With zv = z * z_scale and xv = x_act(x * x_scale):
  *   dz    = dout * act'(zv)
  *   dx    = dz @ w, dw = dz^T @ xv, dbias = sum over rows of dz
- * as mc2_linear_act_grad gives them, which see.  x_act lets the input be kept
+ * as mc2_linear_act_grad gives them, which see; where zv is NaN, so is dz, with
+ * relu too.  x_act lets the input be kept
  * as the pre-activation it came from: a feed-forward's second linear takes
  * the codes of its first one's z.  xv is rounded to dtype for its product, as
  * dz is.

@@ -193,3 +193,18 @@ def test_graph_replay(mc2):
         torch.cuda.synchronize()
         for a, c in zip(out, step()):
             assert torch.equal(a, c)
+
+
+def test_a_group_that_is_nan_says_so(mc2):
+    """Values that come back as NaN have a NaN in their gradients under every activation, relu's included."""
+    m, k, n = 5, 64, 256
+    w, dout = rand(71, n, k).cuda(), rand(72, m, n).cuda()
+    xc, xs = mc2.mc2_quant_rows(rand(73, m, k).cuda(), group=128)
+    z = rand(74, m, n)
+    z[2, 3] = float("nan")
+    zc, zs = mc2.mc2_quant_rows(z.cuda(), group=128)
+    for code in range(1, 5):
+        dx, dw, db = mc2.mc2_linear_act_grad_i8(dout, xc, xs, w, zc, zs, act=code, need_dbias=True)
+        assert torch.isnan(dx[2]).all() and torch.isfinite(dx[[0, 1, 3, 4]]).all(), code
+        assert torch.isnan(dw[:128]).all() and torch.isfinite(dw[128:]).all(), code
+        assert torch.isnan(db[:128]).all() and torch.isfinite(db[128:]).all(), code
