@@ -28,9 +28,17 @@ __device__ __forceinline__ u32x2 load_codes(const int8_t* row, int64_t c, int64_
   }
   return v;
 }
+// -128 under a negative scale is -inf (MC2_KEEP_INF): as fp32's lowest number, of
+// which the activations and their slopes are what they tend to (of -inf itself
+// a product is -inf * 0), and which rounds to -inf in 16 bits.
 __device__ __forceinline__ void code_values(u32x2 v, float scale, float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; e++) f[e] = (float)(int8_t)(v[e / 4] >> (8 * (e & 3))) * scale;
+  if (scale < 0.0f) {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if ((v[e / 4] >> (8 * (e & 3)) & 0xFFu) == 0x80u) f[e] = -3.402823466e38f;
+  }
 }
 // Which scale of its row column c has (group 0: the only one; 128).
 __device__ __forceinline__ int64_t scale_at(int64_t c, int64_t group) { return group ? c / 128 : 0; }

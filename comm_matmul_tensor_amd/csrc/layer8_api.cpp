@@ -77,6 +77,8 @@ mc2_status mc2_moe_route_grad(const float* dweights, const void* logits, const i
 mc2_status mc2_quant_rows(const void* x, int64_t rows, int64_t cols, mc2_dtype dtype, int64_t group, int8_t* codes,
                           float* scale, void* stream) {
   clear_error();
+  const bool keep_inf = group == 128 + MC2_KEEP_INF;
+  if (keep_inf) group = 128;
   mc2_status s = check_code_rows("quant_rows", x, codes, scale, rows, cols, dtype, group, MC2_ACT_NONE);
   if (s != MC2_OK || rows == 0) return s;
   int dev;
@@ -89,6 +91,7 @@ mc2_status mc2_quant_rows(const void* x, int64_t rows, int64_t cols, mc2_dtype d
   a.cols = cols;
   a.group = group;
   a.dtype = dtype;
+  a.keep_inf = keep_inf;
   return launched(launch_quant_rows(a, static_cast<hipStream_t>(stream)), "quant_rows launch");
 }
 

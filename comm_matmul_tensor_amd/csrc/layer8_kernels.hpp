@@ -32,6 +32,7 @@ struct CodeArgs {
   int64_t rows, cols, group;
   int64_t ld;                // columns between the rows written (dequant): 0 means cols; those past cols become 0
   int dtype, act;
+  bool keep_inf;             // quant, group 128: MC2_KEEP_INF
 };
 hipError_t launch_quant_rows(const CodeArgs& a, hipStream_t s);
 hipError_t launch_dequant_rows(const CodeArgs& a, hipStream_t s);

@@ -14,7 +14,9 @@ stay on the stream they were made on, which a capture may not touch).
 With `keep8` a block keeps its linears' input and pre-activation for the
 backward as int8 codes with a scale per 128 columns, and no activation: per
 token h + hidden bytes where it would keep 2 h + 4 hidden.  The forward is the
-same; the gradients are those at the codes' values.
+same; the gradients are those at the codes' values (of a pre-activation that
+overflowed to -inf, 0, as in 16 bits; one of +inf, which leaves no finite
+output, counts as the largest finite of its 128 columns).
 
 ``Int8FeedForward`` and ``Int8ExpertsFeedForward`` serve a trained block with
 int8 codes for its weights (a scale per output channel) and its activations
@@ -94,7 +96,9 @@ class KeptLinearsFunction(torch.autograd.Function):
     def forward(ctx, x, w1, b1, w2, b2, residual, act: int, group_offsets):
         a, z = mc2_linear_act(x, w1, b1, act=act, group_offsets=group_offsets, need_z=True)
         out, _ = mc2_linear_act(a, w2, b2, residual, act=MC2_ACT_NONE, group_offsets=group_offsets)
-        ctx.save_for_backward(*mc2_quant_rows(x, group=128), *mc2_quant_rows(z, group=128), w1, w2, group_offsets)
+        # a pre-activation past its 16 bits' range is an infinity, which is to cost the other columns nothing
+        inf = dict(keep_inf=True) if z.element_size() == 2 else {}
+        ctx.save_for_backward(*mc2_quant_rows(x, group=128), *mc2_quant_rows(z, group=128, **inf), w1, w2, group_offsets)
         ctx.act, ctx.biases, ctx.has_residual = act, (b1 is not None, b2 is not None), residual is not None
         return out
 

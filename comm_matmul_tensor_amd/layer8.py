@@ -19,6 +19,7 @@ from .layer import (_F32, _FLT, _HALF, _I32, _SZ, _SZP, MC2_ACT_NONE, _half, _li
                     _ptr, _tensor, _workspace_ok)
 
 MC2_SCORE_SOFTMAX, MC2_SCORE_SIGMOID = range(2)
+MC2_KEEP_INF = 1 << 16
 
 _SIGS = {
     "mc2_moe_route": [_P, _P, _I64, _I64, _I64, _INT, _INT, _I64, _I64, _I64, _INT, _FLT, _P, _P, _P],
@@ -132,18 +133,23 @@ def _scales(cols: int, group: int) -> int:
     return -(-cols // 128) if group else 1
 
 
-def mc2_quant_rows(x: torch.Tensor, *, group: int = 0, codes: Optional[torch.Tensor] = None,
+def mc2_quant_rows(x: torch.Tensor, *, group: int = 0, keep_inf: bool = False, codes: Optional[torch.Tensor] = None,
                    scale: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(int8 codes of x's shape, fp32 scale): max |x| / 127 per row of x's last dimension (group 0, scale (..., 1)) or
-    per 128 of its columns (group 128, scale (..., ceil(columns / 128))), and rint(x / scale)."""
+    per 128 of its columns (group 128, scale (..., ceil(columns / 128))), and rint(x / scale).
+
+    A group with an infinity or a NaN comes back as NaN.  With keep_inf (group 128; for pre-activations) infinities
+    do not count for the scale: +inf becomes the largest finite value of its group, and -inf stays one."""
     if stream is not None:
-        return _on(stream, mc2_quant_rows, x, group=group, codes=codes, scale=scale)
+        return _on(stream, mc2_quant_rows, x, group=group, keep_inf=keep_inf, codes=codes, scale=scale)
     shape = _tensor(x, "x")
     if len(shape) < 1:
         raise ValueError("x must have a last dimension")
     _half(x, "x")
     if group not in (0, 128):
         raise ValueError(f"group must be 0 or 128, got {group}")
+    if keep_inf and group != 128:
+        raise ValueError("keep_inf needs group 128")
     cols = shape[-1]
     scales = (*shape[:-1], _scales(cols, group))
     if codes is not None:
@@ -155,8 +161,8 @@ def mc2_quant_rows(x: torch.Tensor, *, group: int = 0, codes: Optional[torch.Ten
         codes = x.new_empty(shape, dtype=_I8)
     if scale is None:
         scale = x.new_empty(scales, dtype=_F32)
-    _check(_lib.mc2_quant_rows(x.data_ptr(), x.numel() // cols if cols else 0, cols, _TORCH_DT[x.dtype], group,
-                               codes.data_ptr(), scale.data_ptr(), handle))
+    _check(_lib.mc2_quant_rows(x.data_ptr(), x.numel() // cols if cols else 0, cols, _TORCH_DT[x.dtype],
+                               group + MC2_KEEP_INF if keep_inf else group, codes.data_ptr(), scale.data_ptr(), handle))
     return codes, scale
 
 
@@ -304,5 +310,5 @@ def mc2_linear_act_grad_i8(dout: torch.Tensor, x: torch.Tensor, x_scale: torch.T
     return dx, dw, dbias
 
 
-__all__ = ["MC2_SCORE_SOFTMAX", "MC2_SCORE_SIGMOID", "mc2_moe_route", "mc2_moe_route_grad", "mc2_quant_rows",
+__all__ = ["MC2_SCORE_SOFTMAX", "MC2_SCORE_SIGMOID", "MC2_KEEP_INF", "mc2_moe_route", "mc2_moe_route_grad", "mc2_quant_rows",
            "mc2_dequant_rows", "mc2_linear_i8", "mc2_linear_act_grad_i8"]

@@ -89,11 +89,20 @@ mc2_status mc2_moe_route_grad(const float* dweights, const void* logits, const i
  * x (rows, cols) of dtype (MC2_F16 or MC2_BF16), codes (rows, cols) int8,
  * scale (rows, ceil(cols / group)) fp32 (group 0: (rows, 1)).
  * rows < 2^24, 1 <= cols <= 2^24.
+ *
+ * group = 128 + MC2_KEEP_INF: as 128, for pre-activations, which their 16 bits
+ * may hold as infinities.  a is the largest finite |x| of the group (if that is
+ * 0 and an infinity is there, the type's largest number); +inf gets the code
+ * of a.  -inf, whose activation and slope are 0, stays one: a group with a -inf
+ * has the negative scale -a / 127 (and the codes rint(x / scale) of that), and
+ * the code -128 for it.  In mc2_dequant_rows and mc2_linear_act_grad_i8 a code
+ * of -128 under a negative scale is -inf.
  */
+enum { MC2_KEEP_INF = 1 << 16 };
 mc2_status mc2_quant_rows(const void* x, int64_t rows, int64_t cols, mc2_dtype dtype, int64_t group, int8_t* codes,
                           float* scale, void* stream);
 
-/* And back: out = act(code * scale), rounded once to dtype.  Arguments as in mc2_quant_rows. */
+/* And back: out = act(code * scale), rounded once to dtype.  Arguments as in mc2_quant_rows (group 0 or 128). */
 mc2_status mc2_dequant_rows(const int8_t* codes, const float* scale, int64_t rows, int64_t cols, int64_t group,
                             mc2_act act, mc2_dtype dtype, void* out, void* stream);
 
@@ -126,10 +135,9 @@ mc2_status mc2_linear_i8(const int8_t* x, const float* x_scale, const int8_t* w,
  *   dz    = dout * act'(zv)
  *   dx    = dz @ w, dw = dz^T @ xv, dbias = sum over rows of dz
  * as mc2_linear_act_grad gives them, which see; where zv is NaN, so is dz, with
- * relu too.  x_act lets the input be kept
- * as the pre-activation it came from: a feed-forward's second linear takes
- * the codes of its first one's z.  xv is rounded to dtype for its product, as
- * dz is.
+ * relu too.  x_act lets the input be kept as the pre-activation it came from: a
+ * feed-forward's second linear takes the codes of its first one's z.  xv is
+ * rounded to dtype for its product, as dz is.
  * x (m, k) int8, x_scale (m, ceil(k / 128)) fp32 (needed for dw alone);
  * z (m, n) int8, z_scale (m, ceil(n / 128)) fp32 (NULL with MC2_ACT_NONE);
  * dout, w, dx, dw, dbias of dtype.

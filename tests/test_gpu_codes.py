@@ -138,3 +138,60 @@ def test_offsets_past_32_bits(mc2):
         v = ref.values(want, ws, group)
         check(back[-4:], v, rounded(v, "bf16") * 1.01, "back")
         x[-4:] = tail.cuda()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("cols", [128, 300, 1024, 4099])
+def test_infinities_that_are_kept(mc2, dtype, cols):
+    """keep_inf: the scale is that of the finite values (the type's largest number where there are none but zeros), +inf
+    takes its place at the end of the range, -inf comes back as one; finite groups are those of group 128 bit for bit,
+    and a NaN still makes its group NaN."""
+    big = 65504.0 if dtype == "f16" else torch.finfo(torch.bfloat16).max
+    x = rand(cols, 12, cols, std=2.0, dtype=dtype)
+    inf = math.inf
+    x[1, 5] = -inf
+    x[2, 5], x[2, 77], x[2, 127] = inf, inf, 0.0
+    x[3, 5], x[3, 6] = -inf, inf
+    x[4, :128] = -inf
+    x[5, :128] = 0.0
+    x[5, 17], x[5, 99] = -inf, inf
+    x[6, :128] = inf
+    x[7, 5], x[7, 6] = math.nan, -inf
+    x[8, cols - 1] = -inf                      # the last group, which may be short
+    x[9, ::2] = -inf
+    x[10, :128] = -0.0
+    codes, scale = mc2.mc2_quant_rows(x.cuda(), group=128, keep_inf=True)
+    codes, scale = codes.cpu(), scale.cpu()
+    plain = mc2.mc2_quant_rows(x.cuda(), group=128)
+    back = {name: mc2.mc2_dequant_rows(codes.cuda(), scale.cuda(), group=128, act=ACTS.index(name), dtype=DT[dtype]).cpu()
+            for name in ACTS}
+    for r in range(12):
+        for g in range(scale.shape[1]):
+            at = slice(128 * g, min(128 * g + 128, cols))
+            v, c, s = x[r, at].float(), codes[r, at], scale[r, g]
+            if torch.isnan(v).any():
+                assert torch.isnan(s) and torch.count_nonzero(c) == 0
+                assert all(torch.isnan(b[r, at]).all() for b in back.values())
+                continue
+            low, lost = v == -inf, torch.isinf(v)
+            if not lost.any():
+                assert torch.equal(c, plain[0][r, at].cpu()) and s == plain[1][r, g].cpu()
+                continue
+            top = v[~lost].abs().max() if (~lost).any() else torch.zeros(())
+            top = top if top > 0 else torch.tensor(big)
+            want = -(top / 127) if low.any() else top / 127
+            assert s == want, (r, g)
+            q = torch.round(v.clamp(-float(top), float(top)) / want).to(torch.int8)
+            q[low] = -128
+            assert torch.equal(c, q), (r, g)
+            assert (back["none"][r, at][low] == -inf).all()
+            assert torch.equal(torch.isinf(back["none"][r, at]), low) or top == big
+            for name in ACTS[1:]:
+                assert (back[name][r, at][low] == 0).all() and not torch.isnan(back[name][r, at]).any(), name
+
+
+def test_no_infinity_no_difference(mc2):
+    for rows, cols in ((1, 1), (3, 131), (70, 2048), (2, 7168)):
+        x = rand(rows + cols, rows, cols).cuda()
+        for a, b in zip(mc2.mc2_quant_rows(x, group=128), mc2.mc2_quant_rows(x, group=128, keep_inf=True)):
+            assert torch.equal(a, b)

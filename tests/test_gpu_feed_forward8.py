@@ -280,3 +280,50 @@ def test_state_moves_with_the_module(ff):
     assert not torch.equal(a(x)[0], b(x)[0])
     b.load_state_dict(a.state_dict())
     assert torch.equal(a(x)[0], b(x)[0])
+
+
+@pytest.mark.parametrize("act_name", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_an_overflowed_pre_activation_keeps_its_neighbours(ff, act_name):
+    """z past fp16's range is saved as -inf, whose activation and slope are 0.  It stays one among the codes, and its 128
+    columns keep those of their finite values; the gradients are those of the formula at these values (near()'s
+    bound, of the coarser type)."""
+    import comm_matmul_tensor_amd as mc2
+    from layer_ref import ACTS
+    torch.manual_seed(12)
+    code = ACTS.index(act_name)
+    block = ff.FeedForward(192, 400, act=code, dtype=torch.float16, keep8=True)
+    with torch.no_grad():
+        block.b1.copy_(torch.linspace(-0.5, 0.5, 400))
+        for col in (5, 130, 399):
+            block.b1[col] = -65504.0
+            block.w1[col].zero_()
+            block.w1[col, 0] = -400.0  # -inf where the row's first value is 1, else finite
+        block.b1[256:384] = -65504.0   # a group of nothing else
+        block.w1[256:384].zero_()
+        block.w1[256:384, 1] = -400.0
+    x = torch.randn((77, 192), device="cuda").half()
+    x[:, 0], x[:, 1] = 1.0, 1.0
+    x[40:] = -x[40:].abs()             # these rows are finite
+    x.requires_grad_()
+    d = torch.randn((77, 192), device="cuda").half()
+    out = block(x)
+    assert torch.isfinite(out).all()
+    out.backward(d)
+    with torch.no_grad():
+        y = mc2.mc2_add_rms_norm(x, block.norm)[0]
+        z = mc2.mc2_linear_act(y, block.w1, block.b1, act=code, need_z=True)[1].cpu()
+    low = z == -float("inf")
+    assert low[:40, 5].all() and low[:40, 256:384].all() and not low[40:].any() and torch.isfinite(z[~low]).all()
+    zk = ref.values(*ref.codes(torch.where(low, torch.zeros_like(z), z), 128), 128)
+    zk[low] = -1e4
+    p = {k: leaf(v) for k, v in block.named_parameters()}
+    xr = leaf(x)
+    yk = at_codes(norm64(xr, p["norm"], 1e-6), kept_values(mc2, y))
+    zr = at_codes(yk @ p["w1"].T + p["b1"], zk)
+    # (relu's slope at a value of 0, which many codes are, is 0; autograd's of the clamp in act() is 1)
+    ar = torch.relu(zr) if act_name == "relu" else act(zr, act_name)[0]
+    want = xr + ar @ p["w2"].T + p["b2"]
+    want.backward(d.cpu().double())
+    near(x.grad, xr.grad, "x")
+    for k, v in block.named_parameters():
+        near(v.grad, p[k].grad, k)

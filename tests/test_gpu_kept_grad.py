@@ -208,3 +208,41 @@ def test_a_group_that_is_nan_says_so(mc2):
         assert torch.isnan(dx[2]).all() and torch.isfinite(dx[[0, 1, 3, 4]]).all(), code
         assert torch.isnan(dw[:128]).all() and torch.isfinite(dw[128:]).all(), code
         assert torch.isnan(db[:128]).all() and torch.isfinite(db[128:]).all(), code
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_a_pre_activation_of_minus_infinity(mc2, dtype):
+    """Kept with keep_inf its slope and its activation are 0 and its neighbours' what they are without it: the
+    gradients of the formula where its dz and its column of the second linear's input are cleared."""
+    m, k, n = 40, 136, 264
+    u = U[dtype]
+    w1, w2 = rand(81, n, k, std=k ** -0.5, dtype=dtype), rand(82, k, n, std=n ** -0.5, dtype=dtype)
+    x, dout, z = rand(83, m, k, dtype=dtype), rand(84, m, n, dtype=dtype), rand(85, m, n, std=1.5, dtype=dtype)
+    zero = z.clone()
+    z[3, 5], z[3, 130], z[20, 263], z[39, :128] = -float("inf"), -float("inf"), -float("inf"), -float("inf")
+    low = torch.isinf(z)
+    zero[low] = 0.0
+    xc, xs = mc2.mc2_quant_rows(x.cuda(), group=128)
+    zc, zs = mc2.mc2_quant_rows(z.cuda(), group=128, keep_inf=True)
+    v = ref.values(*ref.codes(zero, 128), 128)
+    for name in ACTS[1:]:
+        a, slope = act(v, name)
+        a[low], slope[low] = 0.0, 0.0
+        code = ACTS.index(name)
+        dx, dw, db = mc2.mc2_linear_act_grad_i8(dout.cuda(), xc, xs, w1.cuda(), zc, zs, act=code, need_dbias=True)
+        dz, xv = dout.double() * slope, ref.values(xc.cpu(), xs.cpu(), 128)
+        # dz and the input are rounded to 16 bits, their sums in fp32; a slope is within ACT_ERR (1 + |z|)^3
+        ez = (ACT_ERR * (1 + v.abs()) ** 3 + 4 * EPS32) * dout.double().abs() + u * dz.abs() + TINY[dtype]
+        ez[low] = 0.0
+        r = dz @ w1.double()
+        check(dx, r, rounded(r, dtype) + (1 + u) * (ez + n * EPS32 * dz.abs()) @ w1.double().abs(), name)
+        r = dz.T @ xv
+        check(dw, r, rounded(r, dtype) + (1 + u) * ((ez + m * EPS32 * dz.abs()).T @ xv.abs() * (1 + u) +
+                                                    dz.abs().T @ (u * xv.abs() + TINY[dtype])), name)
+        r = dz.sum(0)
+        check(db, r, rounded(r, dtype) + (1 + u) * (ez + (m + 8) * EPS32 * dz.abs()).sum(0), name)
+        d2 = rand(86, m, k, dtype=dtype)
+        _, dw2, _ = mc2.mc2_linear_act_grad_i8(d2.cuda(), zc, zs, w2.cuda(), x_act=code, need_dx=False)
+        r = d2.double().T @ a
+        ea = ACT_ERR * (1 + v.abs()) + 1.13 * EPS32 * v.abs() + u * a.abs() + TINY[dtype]
+        check(dw2, r, rounded(r, dtype) + (1 + u) * d2.double().abs().T @ (ea + (m + 4) * EPS32 * a.abs()), name)

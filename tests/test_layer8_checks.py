@@ -236,3 +236,18 @@ def test_plan_hook():
     assert plan(I(1), I(4096), I(4096), I(0), ctypes.byref(tile), ctypes.byref(splits)) == OK and tile.value < 0
     assert plan(I(64), I(4096), I(4096), I(0), NULL, ctypes.byref(splits)) == ERR_NULL
     assert plan(I(64), I(1 << 17), I(4096), I(0), ctypes.byref(tile), ctypes.byref(splits)) == ERR_SHAPE
+
+
+def test_keep_inf_is_for_groups_of_128():
+    src = open(HEADER).read()
+    assert re.search(r"MC2_KEEP_INF\s*=\s*1 << 16", src) and mc2.MC2_KEEP_INF == 1 << 16
+    with pytest.raises(ValueError, match="keep_inf needs group 128"):
+        mc2.mc2_quant_rows(W16, keep_inf=True)
+    with pytest.raises(ValueError, match="must be a device tensor"):
+        mc2.mc2_quant_rows(W16, group=128, keep_inf=True)
+    flag = mc2.MC2_KEEP_INF
+    for g in (flag, flag + 64, flag + 256, 2 * flag + 128, 128 - flag):
+        assert lib.mc2_quant_rows(A, I(4), I(256), BF16, I(g), A, A, NULL) == ERR_SHAPE, g
+    assert lib.mc2_quant_rows(NULL, I(0), I(256), BF16, I(flag + 128), NULL, NULL, NULL) == OK
+    assert lib.mc2_quant_rows(A, I(4), I(256), F32, I(flag + 128), A, A, NULL) == ERR_DTYPE
+    assert lib.mc2_dequant_rows(A, A, I(4), I(256), I(flag + 128), 0, BF16, A, NULL) == ERR_SHAPE
