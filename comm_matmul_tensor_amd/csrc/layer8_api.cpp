@@ -28,6 +28,8 @@ mc2_status mc2_moe_route(const void* logits, const float* bias, int64_t tokens, 
                          mc2_dtype dtype, mc2_score score, int64_t groups, int64_t top_groups, int64_t group_top,
                          int renormalise, float scale, int32_t* expert_ids, float* weights, void* stream) {
   clear_error();
+  const bool keep_nan = score == MC2_SCORE_KEEP_NAN + MC2_SCORE_SOFTMAX || score == MC2_SCORE_KEEP_NAN + MC2_SCORE_SIGMOID;
+  if (keep_nan) score = (mc2_score)(score - MC2_SCORE_KEEP_NAN);
   mc2_status s = check_moe_route(logits, bias, tokens, experts, top, dtype, score, groups, top_groups, group_top, scale,
                                  expert_ids, weights);
   if (s != MC2_OK || tokens == 0) return s;
@@ -44,6 +46,7 @@ mc2_status mc2_moe_route(const void* logits, const float* bias, int64_t tokens, 
   a.groups = (int)groups;
   a.top_groups = (int)top_groups;
   a.group_top = (int)group_top;
+  a.keep_nan = keep_nan;
   a.renormalise = renormalise != 0;
   a.scale = scale;
   a.ids = expert_ids;

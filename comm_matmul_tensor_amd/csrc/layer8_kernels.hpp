@@ -13,6 +13,7 @@ struct RouteArgs {
   int64_t tokens;
   int experts, top, dtype, score;
   int groups, top_groups, group_top, renormalise;
+  bool keep_nan;       // a token without a usable logit: its experts are 0 .. top - 1, not -1
   float scale;
   int32_t* ids;        // read by the gradient
   float* weights;

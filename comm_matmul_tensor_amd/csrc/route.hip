@@ -561,7 +561,7 @@ __global__ __launch_bounds__(64 * kWaves) void route_kernel(RouteArgs a, Spread 
   if (chosen) w = softmax ? exp_near<true>(v - m) : v < kNoSigmoid ? 0.0f : Sigmoid::of(v, m).p;
   if (a.renormalise) sum = team_sum<TEAM>(w);
   if (there && lane < a.top) {
-    a.ids[token * a.top + lane] = wrong ? -1 : id;
+    a.ids[token * a.top + lane] = !wrong ? id : a.keep_nan ? lane : -1;
     a.weights[token * a.top + lane] = wrong ? __builtin_nanf("") : w > 0.0f ? a.scale * (w / sum) : 0.0f;
   }
 }

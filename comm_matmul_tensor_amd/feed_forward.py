@@ -203,7 +203,10 @@ class ExpertsFeedForward(torch.nn.Module):
 
     With a `score` (MC2_SCORE_SOFTMAX or MC2_SCORE_SIGMOID) the choice is mc2_moe_route's: experts in `groups`,
     of which top_groups are kept by the sum of their group_top best, weights renormalised and scaled.  `balance`
-    adds the buffer `bias` (experts) fp32 to the scores in the choice alone, for the caller to move."""
+    adds the buffer `bias` (experts) fp32 to the scores in the choice alone, for the caller to move.
+
+    A token with a NaN among its logits, or under a softmax one of +inf (past fp16's range), leaves as a row of NaN; one
+    whose experts are all off (a bias of -inf) as a row of 0."""
 
     def __init__(self, h: int, hidden: int, experts: int, top: int, act: int = MC2_ACT_SILU, eps: float = 1e-6,
                  dtype=torch.bfloat16, device="cuda", keep8: bool = False, score: Optional[int] = None,
@@ -212,7 +215,8 @@ class ExpertsFeedForward(torch.nn.Module):
         super().__init__()
         self.experts, self.top, self.act, self.eps, self.keep8 = experts, top, act, eps, keep8
         self.kind = None if score is None else dict(score=score, groups=groups, top_groups=top_groups,
-                                                    group_top=group_top, renormalise=renormalise, scale=scale)
+                                                    group_top=group_top, renormalise=renormalise, scale=scale,
+                                                    keep_nan=True)
         if score is None and (groups, top_groups, group_top, renormalise, scale, balance) != (1, 1, 1, True, 1.0, False):
             raise ValueError("groups, weights and a balancing bias need a score")
         kw = dict(dtype=dtype, device=device)

@@ -19,7 +19,7 @@ from .layer import (_F32, _FLT, _HALF, _I32, _SZ, _SZP, MC2_ACT_NONE, _half, _li
                     _ptr, _tensor, _workspace_ok)
 
 MC2_SCORE_SOFTMAX, MC2_SCORE_SIGMOID = range(2)
-MC2_KEEP_INF = 1 << 16
+MC2_SCORE_KEEP_NAN = MC2_KEEP_INF = 1 << 16
 
 _SIGS = {
     "mc2_moe_route": [_P, _P, _I64, _I64, _I64, _INT, _INT, _I64, _I64, _I64, _INT, _FLT, _P, _P, _P],
@@ -69,19 +69,22 @@ def _codes(t, name: str):
 # ------------------------------------------------------------------ router
 def mc2_moe_route(logits: torch.Tensor, top: int, bias: Optional[torch.Tensor] = None, *,
                   score: int = MC2_SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1, group_top: int = 1,
-                  renormalise: bool = True, scale: float = 1.0, expert_ids: Optional[torch.Tensor] = None,
-                  weights: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+                  renormalise: bool = True, scale: float = 1.0, keep_nan: bool = False,
+                  expert_ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None, stream=None
+                  ) -> Tuple[torch.Tensor, torch.Tensor]:
     """(expert_ids (tokens, top) int32, weights (tokens, top) fp32) of logits (tokens, experts), fp32 or 16-bit.
 
     The `top` experts of the largest score + bias, in descending order (equal ones: the lowest first; without a bias by
     their logits, also where the scores round to equal numbers); the weights are their scores (without the bias)
     times scale, with renormalise over their sum.  groups > 1: only experts of the top_groups groups of neighbours
     whose group_top (1 or 2) largest sum to most.  A logit of -inf turns an expert off; an id is -1 (weight 0) where
-    too few are on, and all are (weights NaN) for a token with a NaN.
+    too few are on, and all are (weights NaN) for a token with a NaN, or under a softmax a logit of +inf.  With keep_nan
+    such a token has the experts 0 .. top - 1, through which its weights make its row of mc2_moe_unpermute NaN.
     """
     if stream is not None:
         return _on(stream, mc2_moe_route, logits, top, bias, score=score, groups=groups, top_groups=top_groups,
-                   group_top=group_top, renormalise=renormalise, scale=scale, expert_ids=expert_ids, weights=weights)
+                   group_top=group_top, renormalise=renormalise, scale=scale, keep_nan=keep_nan, expert_ids=expert_ids,
+                   weights=weights)
     tokens, experts = _tensor(logits, "logits", 2)
     if logits.dtype not in _LOGITS:
         raise TypeError(f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
@@ -98,8 +101,8 @@ def mc2_moe_route(logits: torch.Tensor, top: int, bias: Optional[torch.Tensor] =
         expert_ids = logits.new_empty((tokens, top), dtype=_I32)
     if weights is None:
         weights = logits.new_empty((tokens, top), dtype=_F32)
-    _check(_lib.mc2_moe_route(logits.data_ptr(), _ptr(bias), tokens, experts, top, _TORCH_DT[logits.dtype], score,
-                              groups, top_groups, group_top, bool(renormalise), scale, expert_ids.data_ptr(),
+    _check(_lib.mc2_moe_route(logits.data_ptr(), _ptr(bias), tokens, experts, top, _TORCH_DT[logits.dtype],
+                              score + MC2_SCORE_KEEP_NAN if keep_nan else score, groups, top_groups, group_top, bool(renormalise), scale, expert_ids.data_ptr(),
                               weights.data_ptr(), handle))
     return expert_ids, weights
 
@@ -310,5 +313,5 @@ def mc2_linear_act_grad_i8(dout: torch.Tensor, x: torch.Tensor, x_scale: torch.T
     return dx, dw, dbias
 
 
-__all__ = ["MC2_SCORE_SOFTMAX", "MC2_SCORE_SIGMOID", "MC2_KEEP_INF", "mc2_moe_route", "mc2_moe_route_grad", "mc2_quant_rows",
+__all__ = ["MC2_SCORE_SOFTMAX", "MC2_SCORE_SIGMOID", "MC2_SCORE_KEEP_NAN", "MC2_KEEP_INF", "mc2_moe_route", "mc2_moe_route_grad", "mc2_quant_rows",
            "mc2_dequant_rows", "mc2_linear_i8", "mc2_linear_act_grad_i8"]

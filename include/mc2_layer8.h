@@ -24,7 +24,8 @@ extern "C" {
 /* Scores of mc2_moe_route. */
 typedef enum {
   MC2_SCORE_SOFTMAX = 0, /* exp(l) / sum over the experts of exp(l) */
-  MC2_SCORE_SIGMOID = 1  /* 1 / (1 + exp(-l)) */
+  MC2_SCORE_SIGMOID = 1, /* 1 / (1 + exp(-l)) */
+  MC2_SCORE_KEEP_NAN = 1 << 16 /* added to one of them in mc2_moe_route: see there */
 } mc2_score;
 
 /*
@@ -47,7 +48,10 @@ typedef enum {
  *               fp64 (logits below -709.78; of the scores that fp32 alone would
  *               round to 0 renormalise gives the shares that they have)
  * A token with a NaN among its logits, or with softmax a logit of +inf, has no
- * experts: ids -1, weights NaN.  (mc2_moe_permute drops an id of -1.)
+ * experts: ids -1, weights NaN.  (mc2_moe_permute drops an id of -1, and
+ * mc2_moe_unpermute reads no weight of one: such a token's row is 0.)  With
+ * MC2_SCORE_KEEP_NAN added to the score it has the experts 0 .. top - 1, so
+ * that its weights make its row NaN.
  * Else c is compared in fp32 where its error there leaves no doubt about the
  * order, and in fp64 otherwise: the choice is that of fp64.
  *

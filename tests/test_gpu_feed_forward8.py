@@ -327,3 +327,34 @@ def test_an_overflowed_pre_activation_keeps_its_neighbours(ff, act_name):
     near(x.grad, xr.grad, "x")
     for k, v in block.named_parameters():
         near(v.grad, p[k].grad, k)
+
+
+@pytest.mark.parametrize("keep8", [False, True])
+@pytest.mark.parametrize("score", [None, 0, 1])
+def test_a_token_without_a_usable_logit_is_nan(ff, score, keep8):
+    """A NaN among a token's logits, or under a softmax one past fp16's range: its row is NaN whichever way the experts
+    are chosen, trained or served in int8, and the other tokens' rows are what they are without it."""
+    torch.manual_seed(11)
+    kind = {} if score is None else dict(score=score, groups=4, top_groups=2, group_top=2, balance=True)
+    block = ff.ExpertsFeedForward(128, 64, experts=8, top=2, dtype=torch.float16, keep8=keep8, **kind)
+    x = torch.randn((21, 128), device="cuda").half()
+    x[7] = 1.0  # its norm is a row of ones
+    for case in ("nan", "inf"):
+        with torch.no_grad():
+            if case == "nan":
+                block.router[3].copy_(torch.randn((128,), device="cuda") * 128 ** -0.5)
+                x[7, 5] = float("nan")
+            else:
+                x[7, 5] = 1.0
+                block.router[3].fill_(600.0)  # 128 * 600 is past 65504, a random row's sum is not
+        others = [t for t in range(21) if t != 7]
+        gone = case == "nan" or score != 1
+        for module in (block, ff.Int8ExpertsFeedForward(block)):
+            out, s = module(x)
+            alone, _ = module(x[others].contiguous())
+            assert torch.isnan(out[7]).all() if gone else torch.isfinite(out[7]).all(), (case, module)
+            assert torch.equal(out[others], alone), (case, module)
+        if gone:  # its gradients are NaN as well, the other tokens' are not
+            v = x.detach().clone().requires_grad_()
+            block(v)[0].float().sum().backward()
+            assert torch.isnan(v.grad[7]).all() and torch.isfinite(v.grad[others]).all(), case

@@ -380,3 +380,18 @@ def test_saturated_sigmoids_without_a_bias(mc2):
                                    top_groups=l.shape[1] // 16 - 1, group_top=1)
         first = list(range(32, 48)) if score == "softmax" else []
         assert ids[0].tolist() == first + [16, 31, 30] and ids[1].tolist() == first + [16, 17, 18], score
+
+
+def test_tokens_whose_nan_is_kept(mc2):
+    """keep_nan: a token without a usable logit has the first experts and NaN weights; nothing else changes."""
+    for experts, top in ((33, 3), (300, 20)):
+        l = logits_of(experts, 9, experts, "f32")
+        l[1, 32], l[2, 0], l[4, 5], l[6] = math.nan, math.inf, -math.inf, -math.inf
+        for score in (mc2.MC2_SCORE_SOFTMAX, mc2.MC2_SCORE_SIGMOID):
+            ids, w = mc2.mc2_moe_route(l.cuda(), top, score=score)
+            kept, wk = mc2.mc2_moe_route(l.cuda(), top, score=score, keep_nan=True)
+            nan = torch.isnan(w).all(1)
+            assert nan.tolist() == [r == 1 or (r == 2 and score == 0) for r in range(9)]
+            assert (ids[nan] == -1).all() and torch.equal(kept[~nan], ids[~nan]) and (ids[6] == -1).all()
+            assert torch.equal(w[~nan], wk[~nan]) and torch.isnan(wk[nan]).all()
+            assert (kept[nan] == torch.arange(top, device="cuda", dtype=torch.int32)).all()

@@ -251,3 +251,15 @@ def test_keep_inf_is_for_groups_of_128():
     assert lib.mc2_quant_rows(NULL, I(0), I(256), BF16, I(flag + 128), NULL, NULL, NULL) == OK
     assert lib.mc2_quant_rows(A, I(4), I(256), F32, I(flag + 128), A, A, NULL) == ERR_DTYPE
     assert lib.mc2_dequant_rows(A, A, I(4), I(256), I(flag + 128), 0, BF16, A, NULL) == ERR_SHAPE
+
+
+def test_keep_nan_is_for_a_score():
+    assert re.search(r"MC2_SCORE_KEEP_NAN\s*=\s*1 << 16", open(HEADER).read()) and mc2.MC2_SCORE_KEEP_NAN == 1 << 16
+    flag = mc2.MC2_SCORE_KEEP_NAN
+    route = lambda sc, t=16: lib.mc2_moe_route(A if t else NULL, NULL, I(t), I(64), I(4), F32, sc, I(1), I(1), I(1), 1,
+                                               ctypes.c_float(1.0), NULL, A, NULL)
+    assert route(flag) == ERR_NULL and route(flag + 1) == ERR_NULL
+    assert route(flag, 0) == OK and route(flag + 1, 0) == OK
+    for sc in (flag + 2, flag - 1, 2 * flag, -flag, -flag + 1):
+        assert route(sc) == ERR_UNSUPPORTED, sc
+    assert lib.mc2_moe_route_grad(A, A, A, I(16), I(64), I(4), F32, flag, 1, ctypes.c_float(1.0), A, NULL) == ERR_UNSUPPORTED
