@@ -94,8 +94,11 @@ class KeptLinearsFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, w1, b1, w2, b2, residual, act: int, group_offsets):
-        a, z = mc2_linear_act(x, w1, b1, act=act, group_offsets=group_offsets, need_z=True)
+        kept = any(ctx.needs_input_grad)  # (a frozen block on rows that need no gradient has no backward)
+        a, z = mc2_linear_act(x, w1, b1, act=act, group_offsets=group_offsets, need_z=kept)
         out, _ = mc2_linear_act(a, w2, b2, residual, act=MC2_ACT_NONE, group_offsets=group_offsets)
+        if not kept:
+            return out
         # a pre-activation past its 16 bits' range is an infinity, which is to cost the other columns nothing
         inf = dict(keep_inf=True) if z.element_size() == 2 else {}
         ctx.save_for_backward(*mc2_quant_rows(x, group=128), *mc2_quant_rows(z, group=128, **inf), w1, w2, group_offsets)

@@ -358,3 +358,17 @@ def test_a_token_without_a_usable_logit_is_nan(ff, score, keep8):
             v = x.detach().clone().requires_grad_()
             block(v)[0].float().sum().backward()
             assert torch.isnan(v.grad[7]).all() and torch.isfinite(v.grad[others]).all(), case
+
+
+def test_a_frozen_block_keeps_nothing(ff):
+    """With grad mode on, where nothing needs a gradient: the forward's bits, and no saved tensor."""
+    torch.manual_seed(13)
+    for block in (ff.FeedForward(128, 256, keep8=True), ff.ExpertsFeedForward(128, 64, experts=4, top=2, keep8=True)):
+        x = torch.randn((33, 128), device="cuda").bfloat16()
+        want = block(x)
+        block.requires_grad_(False)
+        saved = []
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: saved.append(t) or t, lambda t: t):
+            out = block(x)
+        out, want = (out, want) if isinstance(out, torch.Tensor) else (out[0], want[0])
+        assert saved == [] and not out.requires_grad and torch.equal(out, want)

@@ -115,3 +115,29 @@ def test_a_score_is_needed_for_groups_and_balance():
     assert ff.ExpertsFeedForward(8, 8, 4, 2, device="cpu").bias is None
     block = ff.ExpertsFeedForward(8, 8, 4, 2, device="cpu", score=1, balance=True)
     assert block.bias.shape == (4,) and "bias" in block.state_dict()
+
+
+def test_nothing_is_kept_where_nothing_needs_a_gradient(monkeypatch):
+    """A frozen block on rows that need no gradient, evaluated with grad mode on: no codes, no pre-activation."""
+    made = []
+
+    def codes(x, *, group):
+        made.append(x.shape)
+        return quant_rows(x, group=group)
+
+    wanted = []
+
+    def linear(*args, need_z=False, **kw):
+        wanted.append(need_z)
+        return linear_act(*args, need_z=need_z, **kw)
+
+    monkeypatch.setattr(ff, "mc2_quant_rows", codes)
+    monkeypatch.setattr(ff, "mc2_linear_act", linear)
+    ts = [t.detach() for t in calls()["kept, silu"][1]]
+    out = ff.KeptLinearsFunction.apply(*ts, ff.MC2_ACT_SILU, None)
+    assert not out.requires_grad and made == [] and wanted == [False, False]
+    for live in range(6):
+        made.clear()
+        again = ff.KeptLinearsFunction.apply(*(t.clone().requires_grad_(i == live) for i, t in enumerate(ts)),
+                                             ff.MC2_ACT_SILU, None)
+        assert torch.equal(again, out) and len(made) == 2
