@@ -12,11 +12,16 @@ together, while no eager autograd graph of the same parameters lives (its nodes
 stay on the stream they were made on, which a capture may not touch).
 
 With `keep8` a block keeps its linears' input and pre-activation for the
-backward as int8 codes with a scale per 128 columns, and no activation: per
-token h + hidden bytes where it would keep 2 h + 4 hidden.  The forward is the
-same; the gradients are those at the codes' values (of a pre-activation that
-overflowed to -inf, 0, as in 16 bits; one of +inf, which leaves no finite
-output, counts as the largest finite of its 128 columns).
+backward as int8 codes with a scale per 128 columns, and no activation: per row
+h + hidden bytes where it would keep 2 h + 4 hidden.  A dense block has a row
+per token; an experts block has `top`, and keeps their experts' output (2 h
+bytes a row) and the router's input (2 h a token) besides, with keep8 or
+without: top (3 h + hidden) + 2 h bytes a token, where it would keep top (4 h +
+4 hidden) + 2 h.  To that come the residual stream and small tensors (scales,
+logits, ids, weights).  The forward is the same; the gradients are those at the
+codes' values (of a pre-activation that overflowed to -inf, 0, as in 16 bits;
+one of +inf, which leaves no finite output, counts as the largest finite of its
+128 columns).
 
 ``Int8FeedForward`` and ``Int8ExpertsFeedForward`` serve a trained block with
 int8 codes for its weights (a scale per output channel) and its activations

@@ -372,3 +372,30 @@ def test_a_frozen_block_keeps_nothing(ff):
             out = block(x)
         out, want = (out, want) if isinstance(out, torch.Tensor) else (out[0], want[0])
         assert saved == [] and not out.requires_grad and torch.equal(out, want)
+
+
+def test_kept_bytes_of_experts(ff):
+    """Kept between forward and backward of an experts block per token: for each of its `top` rows codes and scales of
+    h + hidden columns in place of 2 h + 4 hidden bytes, and in either case the experts' output (2 h); the normed
+    rows that the router read (2 h), and small change: logits, ids, maps and weights, the residual stream."""
+    h, hidden, top, experts, tokens = 256, 1024, 4, 8, 1024
+    x = torch.randn((tokens, h), device="cuda").bfloat16().requires_grad_()
+    kept = {}
+    for keep8 in (False, True):
+        block = ff.ExpertsFeedForward(h, hidden, experts, top, keep8=keep8, score=1)
+        own = {p.data_ptr() for p in block.parameters()} | {x.data_ptr()}
+        sizes = {}
+
+        def pack(t):
+            if t.data_ptr() not in own:
+                sizes[t.data_ptr()] = t.numel() * t.element_size()
+            return t
+        with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+            out = block(x)
+        kept[keep8] = sum(sizes.values()) / tokens
+        del out
+    # logits 2 each, ids, row_map and weights 4 each; rstd, and the ranges over all tokens
+    small = 2 * experts + 12 * top + 8
+    scales = 4 * (h + hidden) // 128
+    assert top * (h + hidden + 2 * h) + 2 * h <= kept[True] <= top * (h + hidden + scales + 2 * h) + 2 * h + small + 2 * h
+    assert kept[False] >= top * (2 * h + 4 * hidden + 2 * h) + 2 * h
