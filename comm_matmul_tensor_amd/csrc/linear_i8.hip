@@ -146,7 +146,7 @@ int skinny_waves(int64_t m, int64_t k, int64_t n) {
 
 // Whether up to 32 rows take this product or tiles, whose workgroups share the
 // rows of x among 64 columns.  Here a CU reads the 16 rows of w and the m of x of
-// each of its workgroups at 36 bytes a ns (16 rows, 16384 x 1024: 17.3 us, tiles
+// each of its workgroups at 30 bytes a ns (16 rows, 16384 x 1024: 17.3 us, tiles
 // 11.3; 32 rows 24.3, 12.1), tiles take their plan's time; neither less than
 // HBM's (tiles at a lower rate: 16 rows of 4096 x 28672 32.5 us, here 36.0; 8
 // rows 32.2, 31.2; 1 row 33.3, 28.1).  16 rows of 4096 x 4096 7.5, tiles 10.1; of 4096 x
@@ -177,9 +177,14 @@ hipError_t launch_skinny(const Product& p, int64_t k, hipStream_t s) {
 // 4 bytes can be loaded where they stand, in 16-byte chunks that lie across the
 // lines: 64 rows for 32 experts of 4008 x 2040 55.7 us (149.5 with the copy), 517
 // rows of 1000 x 2000 8.5 (11.7), 8191 of 1000 x 1000 20.8 (25.0).  A step's loads
-// then touch twice the lines, which costs a product bound by its MFMAs about a
-// third of their time, and may be more than the copy: 4095 rows of 4008 x 5000
-// 117.6 (100.4 with the copy), of 1000 x 5000 52.8 (50.1).
+// then touch twice the lines, and the codes past the last chunk are loaded by
+// themselves, which together cost a product bound by its MFMAs about a third of
+// their time, and may be more than the copy: 4095 rows of 4008 x 5000 117.6 (100.4
+// with the copy), of 1000 x 5000 52.8 (50.1).  Rows of a multiple of 16 bytes that is
+// none of 128 have the lines alone against them and are read where they stand at
+// all sizes: 4096 x 4000 -> 5000 99 us (95 with the copy), 2048 x 8208 -> 4096 68
+// (73), 4095 x 4000 -> 1000 25 (30), 8191 rows for 32 experts of 4000 -> 1792 138
+// (201).  Of the largest the copy would be the faster: 8192 x 8176 -> 8192 519 (425).
 bool pads(int64_t m, int64_t k, int64_t n, int64_t groups) {
   const double matrices = (double)std::max<int64_t>(groups, 1);
   const double mfma_us = 2.0 * (double)m * (double)n * (double)k / 2.1e9;

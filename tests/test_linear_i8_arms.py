@@ -126,3 +126,18 @@ def test_results(case, dtype):
     want = y + r.double()
     bound = 1.13 * ez + ACT_ERR * (1 + z.abs()) + EPS32 * (y.abs() + r.double().abs())
     near(out, want, rounded(want, dtype) * (1 + U[dtype]) + bound, "out")
+
+
+def test_rows_of_whole_chunks_are_never_copied():
+    """Widths of a multiple of 16 bytes, whole cache lines or not, and widths of no multiple of 4 for comparison."""
+    for m, n, groups in ((4096, 5000, 0), (4095, 1000, 0), (8192, 8192, 0), (8191, 1792, 32), (64, 2048, 32)):
+        for k in (1008, 4000, 4080, 4096, 8176):
+            assert space(m, k, n, groups) < (m + max(groups, 1) * n) * k, (m, k, n, groups)
+            assert space(m, k + 1, n, groups) >= (m + max(groups, 1) * n) * k, (m, k + 1, n, groups)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(1000, 4000, 1000, 0), (4096, 4000, 640, 0), (33, 4080, 200, 0), (700, 4000, 264, 5),
+                                  (2000, 1008, 520, 3)], ids=lambda c: "-".join(map(str, c)))
+def test_results_of_widths_across_the_lines(case):
+    test_results((*case, "", 1), "bf16")
