@@ -11,7 +11,7 @@
 // latency, not by memory (8.4 MB at the copy's rate would take 2 us): 8191
 // tokens x 256 fp32 logits, top 8: 6.6 us in a graph of such calls, where an
 // empty kernel takes 3; with bias 8.9, with 16 groups of which 6 are kept too
-// 12.  (A wavefront a token, its rounds by ballots: 8.6 and 19; loads each
+// 12.4.  (A wavefront a token, its rounds by ballots: 8.6 and 19; loads each
 // under a condition, which are waited for one by one: 11 and 22.)
 //
 // Order.  Without a bias the keys are the logits themselves: p rises with l,
@@ -19,7 +19,7 @@
 // fp32 with an error bound (Doubt).  Where two neighbours of the order lie
 // within it, a tie among them, fp64 decides: on the chosen and the next few
 // alone where that is enough (order64), else on the whole row (choose64), 3
-// us for the few rows of a batch that need it (8191 rows of equal logits: 25).  So
+// us for the few rows of a batch that need it (8191 rows of equal logits: 23).  So
 // the experts chosen are those of fp64, at fp32's cost; bf16 logits under a
 // bias of zeros, which tie in many rows, take 10 us.
 #include "layer8_kernels.hpp"
@@ -109,7 +109,6 @@ __device__ __forceinline__ float team_sum(float v) {
   v += __uint_as_float(dpp16<2>(__float_as_uint(v)));
   return v + __uint_as_float(dpp16<3>(__float_as_uint(v)));
 }
-// f over the wavefront's doubles, as a scalar.
 template <int STEP>
 __device__ __forceinline__ double dpp16d(double v) {
   const u32x2 b = __builtin_bit_cast(u32x2, v);
@@ -120,6 +119,7 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
   return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)b[0], lane),
                                           (uint32_t)__builtin_amdgcn_readlane((int)b[1], lane)});
 }
+// f over the wavefront's doubles, as a scalar.
 template <typename F>
 __device__ __forceinline__ double wave_fold(double v, F f) {
   v = f(v, dpp16d<0>(v));
