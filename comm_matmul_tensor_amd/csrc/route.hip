@@ -246,9 +246,9 @@ __device__ __forceinline__ void groups_of(float inv_per, int (&group)[SLOTS]) {
 // How groups are spread: 2^shift lanes of the team share one (one where there
 // are more than half as many as lanes); a lane's i-th group is i TEAM / 2^shift
 // past its first.  In LDS a token has its groups' values, `quads` of four, their
-// slack, as many, then its scores, a row of per or per + 1 for each group: odd, so that the rows start
-// in different banks (odd_mask: -1 where one is added); then a place that is
-// written only.
+// slack, as many, then its scores, a row of per or per + 1 for each group: odd,
+// so that the rows start in different banks (odd_mask: -1 where one is added);
+// then a place that is written only.
 struct Spread {
   int per, odd_mask, quads, shift, size;  // size: numbers that a token takes, a multiple of four
   float inv_per;

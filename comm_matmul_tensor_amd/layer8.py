@@ -102,8 +102,8 @@ def mc2_moe_route(logits: torch.Tensor, top: int, bias: Optional[torch.Tensor] =
     if weights is None:
         weights = logits.new_empty((tokens, top), dtype=_F32)
     _check(_lib.mc2_moe_route(logits.data_ptr(), _ptr(bias), tokens, experts, top, _TORCH_DT[logits.dtype],
-                              score + MC2_SCORE_KEEP_NAN if keep_nan else score, groups, top_groups, group_top, bool(renormalise), scale, expert_ids.data_ptr(),
-                              weights.data_ptr(), handle))
+                              score + MC2_SCORE_KEEP_NAN if keep_nan else score, groups, top_groups, group_top,
+                              bool(renormalise), scale, expert_ids.data_ptr(), weights.data_ptr(), handle))
     return expert_ids, weights
 
 
@@ -313,5 +313,5 @@ def mc2_linear_act_grad_i8(dout: torch.Tensor, x: torch.Tensor, x_scale: torch.T
     return dx, dw, dbias
 
 
-__all__ = ["MC2_SCORE_SOFTMAX", "MC2_SCORE_SIGMOID", "MC2_SCORE_KEEP_NAN", "MC2_KEEP_INF", "mc2_moe_route", "mc2_moe_route_grad", "mc2_quant_rows",
-           "mc2_dequant_rows", "mc2_linear_i8", "mc2_linear_act_grad_i8"]
+__all__ = ["MC2_SCORE_SOFTMAX", "MC2_SCORE_SIGMOID", "MC2_SCORE_KEEP_NAN", "MC2_KEEP_INF", "mc2_moe_route",
+           "mc2_moe_route_grad", "mc2_quant_rows", "mc2_dequant_rows", "mc2_linear_i8", "mc2_linear_act_grad_i8"]
